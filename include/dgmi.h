@@ -379,6 +379,124 @@ int moe_dispatch_contiguous_fp8(const dg_tensor* x, const dg_tensor* topk_idx, c
 int moe_combine(const dg_tensor* d, const dg_tensor* slot, const dg_tensor* topk_weights,
                 const dg_tensor* y, hipStream_t stream);
 
+/* score functions of the routing */
+enum {
+  DG_SCORE_SOFTMAX = 0,
+  DG_SCORE_SIGMOID = 1
+};
+
+/*
+ * Expert routing: from the router's logits to the tables that
+ * moe_dispatch_*_fp8 (topk_idx) and moe_combine (topk_weights) read.
+ *   logits       F32 or BF16 [T, E], any row stride; E <= 1024
+ *   bias         NULL, or F32 [E]: added to the scores for the choice only
+ *                (a balance term), never to the weights
+ *   topk_idx     I32 [T, k] out, k <= 64, by falling choice; -1 where fewer
+ *                than k experts can be chosen.  (moe_dispatch_*_fp8 wants it
+ *                contiguous; any row stride is written here.)
+ *   topk_weights F32 [T, k] out, 0 where topk_idx is -1
+ *   score        scores s: DG_SCORE_SOFTMAX or DG_SCORE_SIGMOID of the logits
+ *   n_group, topk_group, group_top
+ *                the experts are n_group equal ranges (at most 64); a group's
+ *                score is the sum of its group_top (1 or 2) best choices s +
+ *                bias, and only the experts of the topk_group best groups can
+ *                be chosen.  n_group = 1: no groups
+ *   renormalize  weights are divided by their sum (sigmoid: s_j / (sum +
+ *                1e-20); softmax: the softmax over the chosen logits)
+ *   scale        factor of every weight
+ * Equal choices go to the lowest index.  An expert whose logit or bias is
+ * -inf cannot be chosen (a token whose logits are all -inf is routed
+ * nowhere); NaN ranks below every number.  A +inf softmax logit makes the
+ * row's weights NaN, and so does a NaN one (with renormalisation: a NaN among
+ * the chosen).  Scores are FP32, each operation rounded once.
+ */
+int moe_route_topk(const dg_tensor* logits, const dg_tensor* bias, const dg_tensor* topk_idx,
+                   const dg_tensor* topk_weights, int32_t score, int32_t n_group, int32_t topk_group,
+                   int32_t group_top, int renormalize, float scale, hipStream_t stream);
+
+/*
+ * Gradient of moe_route_topk's weights with respect to the logits, the choice
+ * taken as given.
+ *   logits, topk_idx, score, renormalize, scale  as moe_route_topk; entries
+ *                of topk_idx outside [0, E) give nothing, an expert named
+ *                twice in a row gets both parts
+ *   grad_weights F32 [T, k], any row stride
+ *   grad_logits  F32 or BF16 [T, E] out, written whole
+ */
+int moe_route_topk_bwd(const dg_tensor* logits, const dg_tensor* topk_idx, const dg_tensor* grad_weights,
+                       const dg_tensor* grad_logits, int32_t score, int renormalize, float scale,
+                       hipStream_t stream);
+
+/*
+ * Append new tokens to a paged FP8 key/value cache, rotating keys (and
+ * queries) by their position on the way.  One kernel.
+ *   k, v         F32 or BF16 [T, Hkv, D], the sequences' new tokens one after
+ *                another; D = 64, 128 or 256
+ *   k_cache, v_cache  E4M3 [pages, Hkv, P, D], P = 16, 32, 64 or 128; any
+ *                strides that are multiples of 16 (innermost 1): pages may be
+ *                laid out head by head or token by token, and the two caches
+ *                may be halves of one pool
+ *   k_scale, v_scale  F32 [pages, Hkv], any strides: the scale of each page
+ *                and head, a power of two
+ *   block_table  I32 [S, max_pages]: the pages of each sequence, in order
+ *   cu_tokens    I32 [S + 1]: sequence s brings tokens cu[s] .. cu[s+1]-1
+ *   start        I32 [S]: how many tokens of it are in the cache already, so
+ *                that token t has position start[s] + t - cu[s]
+ *   cos_sin      NULL, or F32 [positions, rot], 16-byte aligned rows: the
+ *                cosines of the rot/2 angles of a position, then the sines.
+ *                rot is a multiple of 16, at most D; the other elements of a
+ *                head are not rotated.  The pair (x, y) becomes (x cos - y
+ *                sin, y cos + x sin), in FP32
+ *   interleaved  pairs are elements (2j, 2j+1); else (j, j + rot/2)
+ *   q, q_out     both NULL, or q of k's type [T, Hq, D] and q_out BF16 of the
+ *                same shape: q rotated, for paged_attention_fp8
+ * A page that gets its first tokens takes the scale 2^ceil(log2(a / 448)), a
+ * the largest absolute value of what it gets (floored at 1e-4); a page that
+ * holds tokens already takes the larger of that and its present scale, and
+ * its older codes are re-encoded when the scale grows.  Values that are not
+ * finite become NaN codes and do not count for a.  Tokens whose position
+ * lies outside the block table or the rows of cos_sin, or whose page is
+ * outside [0, pages), are dropped (their rows of q_out stay as they are where
+ * the position has no row of cos_sin).  No page may be named for appending by
+ * two sequences.
+ */
+int kv_append_fp8(const dg_tensor* k, const dg_tensor* v, const dg_tensor* k_cache, const dg_tensor* v_cache,
+                  const dg_tensor* k_scale, const dg_tensor* v_scale, const dg_tensor* block_table,
+                  const dg_tensor* cu_tokens, const dg_tensor* start, const dg_tensor* cos_sin,
+                  const dg_tensor* q, const dg_tensor* q_out, int interleaved, hipStream_t stream);
+
+/*
+ * Attention of the n newest tokens of each sequence over its paged FP8 cache.
+ *   q         BF16 [S, n, Hq, D]; out BF16, the same shape.  Strides multiples
+ *             of 8 elements, 16-byte aligned bases
+ *   caches, scales, block_table  as kv_append_fp8; Hq a multiple of Hkv (query
+ *             heads h * Hq / Hkv .. share KV head h).  Scales are positive
+ *             and finite
+ *   seq_lens  I32 [S]: tokens in the cache, the n queries' own included (cut
+ *             to what the block table holds).  Query i stands at position
+ *             seq_lens[s] - n + i
+ *   lse       NULL, or F32 [S, n, Hq] out, any strides: the natural logarithm
+ *             of the sum of exp(scores)
+ *   workspace F32, at least paged_attention_fp8_workspace bytes (NULL if that
+ *             is 0), 16-byte aligned; its contents mean nothing between calls,
+ *             but two calls that may run at once need one each
+ *   scale     factor of the scores
+ *   window    a query sees the window positions up to its own; 0: all of them
+ * Positions past a query's own or before its window, and pages outside
+ * [0, pages), take no part, whatever their memory holds (NaN codes too).  A
+ * query that sees nothing gives 0, with lse -inf.  Weights are rounded to FP16
+ * on their way into the second product, sums and output accumulate in FP32.
+ * The result does not depend on the order in which workgroups run.
+ */
+int paged_attention_fp8(const dg_tensor* q, const dg_tensor* k_cache, const dg_tensor* v_cache,
+                        const dg_tensor* k_scale, const dg_tensor* v_scale, const dg_tensor* block_table,
+                        const dg_tensor* seq_lens, const dg_tensor* out, const dg_tensor* lse,
+                        const dg_tensor* workspace, float scale, int32_t window, hipStream_t stream);
+
+/* Bytes of workspace that paged_attention_fp8 needs for these sizes
+ * (max_tokens = max_pages * P); a pure function of its arguments. */
+int64_t paged_attention_fp8_workspace(int64_t S, int64_t n, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_tokens);
+
 /* Launch configuration chosen for a GEMM (a pure function of the shapes).
  * A GEMM is one launch over all N columns, or two launches in stream order:
  * the first over columns [0, n_split), the second (block_n2 > 0) over

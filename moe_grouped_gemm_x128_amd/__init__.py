@@ -28,5 +28,10 @@ from .binding import (  # noqa: F401
     moe_dispatch_masked_fp8,
     moe_dispatch_contiguous_fp8,
     moe_combine,
+    moe_route_topk,
+    moe_route_topk_bwd,
+    kv_append_fp8,
+    paged_attention_fp8,
+    paged_attention_fp8_workspace,
     query_config,
 )

@@ -15,6 +15,7 @@ LIB_PATH = os.path.join(HERE, "libdgmi.so")
 
 DG_F32, DG_BF16, DG_E4M3, DG_I32 = 0, 1, 2, 3
 DG_OK, DG_INVALID_ARG, DG_UNSUPPORTED, DG_LAUNCH_FAILED = 0, 1, 2, 3
+DG_SCORE_SOFTMAX, DG_SCORE_SIGMOID = 0, 1
 DG_KIND_DENSE, DG_KIND_CONTIGUOUS, DG_KIND_MASKED = 0, 1, 2
 DG_KIND_BF16_MASKED, DG_KIND_BF16_DENSE, DG_KIND_BF16_CONTIGUOUS = 3, 4, 5
 DG_KIND_DENSE_ROWB, DG_KIND_CONTIGUOUS_ROWB, DG_KIND_MASKED_ROWB = 6, 7, 8  # FP8, one B scale per row of B
@@ -45,6 +46,11 @@ ENTRY_POINTS = (
     "moe_dispatch_masked_fp8",
     "moe_dispatch_contiguous_fp8",
     "moe_combine",
+    "moe_route_topk",
+    "moe_route_topk_bwd",
+    "kv_append_fp8",
+    "paged_attention_fp8",
+    "paged_attention_fp8_workspace",
     "dg_query_config",
 )
 
@@ -92,7 +98,7 @@ def load_library(path=None):
         raise RuntimeError(f"libdgmi.so not found at {p}: build it with `python -m moe_grouped_gemm_x128_amd.build`")
     lib = ctypes.CDLL(p)
     T = ctypes.POINTER(DgTensor)
-    vp, i64, i32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32
+    vp, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
     sig = {
         "dg_last_error": ([], ctypes.c_char_p),
         "dgmi_init": ([], ctypes.c_int),
@@ -116,6 +122,11 @@ def load_library(path=None):
         "moe_dispatch_masked_fp8": ([T, T, T, T, T, T, T, ctypes.c_int, vp], ctypes.c_int),
         "moe_dispatch_contiguous_fp8": ([T, T, T, T, T, T, T, i32, ctypes.c_int, vp], ctypes.c_int),
         "moe_combine": ([T, T, T, T, vp], ctypes.c_int),
+        "moe_route_topk": ([T, T, T, T, i32, i32, i32, i32, ctypes.c_int, f32, vp], ctypes.c_int),
+        "moe_route_topk_bwd": ([T, T, T, T, i32, ctypes.c_int, f32, vp], ctypes.c_int),
+        "kv_append_fp8": ([T] * 12 + [ctypes.c_int, vp], ctypes.c_int),
+        "paged_attention_fp8": ([T] * 10 + [f32, i32, vp], ctypes.c_int),
+        "paged_attention_fp8_workspace": ([i64] * 6, i64),
         "dg_query_config": ([i32, i64, i64, i64, i64, ctypes.POINTER(DgConfig)], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
@@ -342,6 +353,69 @@ def moe_combine(d, slot, topk_weights, y, stream=None):
     _check(lib.moe_combine(_ref(describe(d)), _ref(describe(slot)), _ref(describe(topk_weights)), _ref(describe(y)),
                            _stream(stream)))
     return y
+
+
+_SCORES = {"softmax": DG_SCORE_SOFTMAX, "sigmoid": DG_SCORE_SIGMOID}
+
+
+def _score_code(score):
+    if score not in _SCORES:
+        raise ValueError(f"score must be one of {sorted(_SCORES)}, got {score!r}")
+    return _SCORES[score]
+
+
+def moe_route_topk(logits, topk_idx, topk_weights, bias=None, score="softmax", n_group=1, topk_group=1, group_top=1,
+                   renormalize=True, scale=1.0, stream=None):
+    """Choose topk_idx.shape[1] experts per row of logits, with their weights
+    (the tables of moe_dispatch_* and moe_combine).  score "softmax" or
+    "sigmoid"; bias counts for the choice only; groups: the topk_group best of
+    n_group ranges of experts by the sum of their group_top best choices."""
+    lib = load_library()
+    _check(lib.moe_route_topk(_ref(describe(logits)), _ref(describe(bias)), _ref(describe(topk_idx)),
+                              _ref(describe(topk_weights)), _score_code(score), int(n_group), int(topk_group),
+                              int(group_top), int(bool(renormalize)), float(scale), _stream(stream)))
+    return topk_idx, topk_weights
+
+
+def moe_route_topk_bwd(logits, topk_idx, grad_weights, grad_logits, score="softmax", renormalize=True, scale=1.0,
+                       stream=None):
+    """grad_logits from the gradient of moe_route_topk's weights (the choice taken as given)."""
+    lib = load_library()
+    _check(lib.moe_route_topk_bwd(_ref(describe(logits)), _ref(describe(topk_idx)), _ref(describe(grad_weights)),
+                                  _ref(describe(grad_logits)), _score_code(score), int(bool(renormalize)),
+                                  float(scale), _stream(stream)))
+    return grad_logits
+
+
+def kv_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_tokens, start, cos_sin=None, q=None,
+                  q_out=None, interleaved=False, stream=None):
+    """Append the tokens k, v [T, Hkv, D] to the paged FP8 caches
+    [pages, Hkv, P, D] (scales [pages, Hkv]), keys rotated by position with
+    cos_sin [positions, rot]; q [T, Hq, D] is rotated into q_out on the way."""
+    lib = load_library()
+    _check(lib.kv_append_fp8(_ref(describe(k)), _ref(describe(v)), _ref(describe(k_cache)), _ref(describe(v_cache)),
+                             _ref(describe(k_scale)), _ref(describe(v_scale)), _ref(describe(block_table)),
+                             _ref(describe(cu_tokens)), _ref(describe(start)), _ref(describe(cos_sin)),
+                             _ref(describe(q)), _ref(describe(q_out)), int(bool(interleaved)), _stream(stream)))
+    return k_cache, v_cache, k_scale, v_scale
+
+
+def paged_attention_fp8_workspace(S, n, Hq, Hkv, D, max_tokens):
+    """Bytes of workspace paged_attention_fp8 needs (max_tokens = max_pages * P)."""
+    return int(load_library().paged_attention_fp8_workspace(int(S), int(n), int(Hq), int(Hkv), int(D),
+                                                            int(max_tokens)))
+
+
+def paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, out, scale, workspace=None,
+                        lse=None, window=0, stream=None):
+    """Attention of the n newest tokens of each sequence, q [S, n, Hq, D],
+    over its pages of the FP8 caches; lse [S, n, Hq] is optional."""
+    lib = load_library()
+    _check(lib.paged_attention_fp8(_ref(describe(q)), _ref(describe(k_cache)), _ref(describe(v_cache)),
+                                   _ref(describe(k_scale)), _ref(describe(v_scale)), _ref(describe(block_table)),
+                                   _ref(describe(seq_lens)), _ref(describe(out)), _ref(describe(lse)),
+                                   _ref(describe(workspace)), float(scale), int(window), _stream(stream)))
+    return out
 
 
 def query_config(kind, G, M, N, K):

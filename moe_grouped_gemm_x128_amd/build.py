@@ -23,7 +23,7 @@ LIB = os.path.join(HERE, "libdgmi.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-SOURCES = ["abi.cpp", "quant.hip", "gemm.hip", "moe.hip"]
+SOURCES = ["abi.cpp", "quant.hip", "gemm.hip", "moe.hip", "route.hip", "kvcache.hip", "attn.hip"]
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}",
@@ -39,10 +39,14 @@ COMMON_FLAGS = [
     f"-I{CSRC}",
 ]
 
+# flags of single sources: the append's rotation rounds every product and sum
+# on its own (contraction pragmas do not bind under -ffp-contract=fast)
+EXTRA_FLAGS = {"kvcache.hip": ["-ffp-contract=off"]}
+
 
 def _compile(src):
     obj = os.path.join(BUILD, os.path.basename(src) + ".o")
-    cmd = [HIPCC, *COMMON_FLAGS, "-x", "hip", "-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [HIPCC, *COMMON_FLAGS, *EXTRA_FLAGS.get(src, []), "-x", "hip", "-c", os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     # the host pass does not know the device-only packed-fp32 feature; that warning is expected
     noise = "is not a recognized feature for this target"

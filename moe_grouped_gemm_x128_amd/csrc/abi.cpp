@@ -961,6 +961,447 @@ int moe_combine(const dg_tensor* d, const dg_tensor* slot, const dg_tensor* topk
   return check_launch(dgmi::launch_moe_combine(p, stream), fname);
 }
 
+namespace {
+
+// Row indices and weights of the routing: [T, k], unit innermost stride, any row stride.
+int check_routes(const dg_tensor* t, const char* name, int32_t dtype, int64_t T, int64_t k, const char* fname) {
+  DG_TRY(check_basic(t, name, true));
+  DG_TRY(check_dtype(t, name, dtype));
+  if (t->ndim != 2 || t->shape[0] != T || t->shape[1] != k)
+    return fail(DG_INVALID_ARG, "%s: %s must be [T, k] = [%lld, %lld]", fname, name, (long long)T, (long long)k);
+  if (!aligned(t->data, 4)) return fail(DG_INVALID_ARG, "%s: %s must be 4-byte aligned", fname, name);
+  return DG_OK;
+}
+
+// An output whose rows overlap each other would be written by two workgroups.
+int check_rows_apart(const dg_tensor* t, const char* name) {
+  for (int i = 0; i < t->ndim; ++i) {
+    if (t->shape[i] <= 1) continue;
+    int64_t inner = 1;  // elements spanned by the dims of smaller stride
+    for (int j = 0; j < t->ndim; ++j) {
+      if (t->shape[j] == 0) return DG_OK;
+      if (j != i && (t->stride[j] < t->stride[i] || (t->stride[j] == t->stride[i] && j > i)))
+        inner += (t->shape[j] - 1) * t->stride[j];
+    }
+    if (t->stride[i] < inner) return fail(DG_INVALID_ARG, "%s: rows overlap in memory", name);
+  }
+  return DG_OK;
+}
+
+// Logits [T, E] in FP32 or BF16.
+int check_logits(const dg_tensor* t, const char* name, const char* fname) {
+  DG_TRY(check_basic(t, name, true));
+  if (t->dtype != DG_F32 && t->dtype != DG_BF16) return fail(DG_INVALID_ARG, "%s: %s must be F32 or BF16", fname, name);
+  if (t->ndim != 2) return fail(DG_INVALID_ARG, "%s: %s must be [T, E]", fname, name);
+  if (!aligned(t->data, elem_size(t->dtype))) return fail(DG_INVALID_ARG, "%s: %s must be element-aligned", fname, name);
+  return DG_OK;
+}
+
+// Workgroups of one launch of 256 threads each: the grid's threads are counted in 32 bits.
+constexpr int64_t kMaxGroups = (int64_t(1) << 24) - 1;
+
+int check_route_limits(int64_t T, int64_t E, int64_t k, int32_t score, float scale, const char* fname) {
+  if (score != DG_SCORE_SOFTMAX && score != DG_SCORE_SIGMOID)
+    return fail(DG_INVALID_ARG, "%s: score must be DG_SCORE_SOFTMAX or DG_SCORE_SIGMOID (got %d)", fname, score);
+  if (k > E) return fail(DG_INVALID_ARG, "%s: k = %lld choices out of E = %lld experts", fname, (long long)k, (long long)E);
+  if (E > 1024 || k > 64)
+    return fail(DG_UNSUPPORTED, "%s: at most 1024 experts and 64 choices (got %lld, %lld)", fname, (long long)E, (long long)k);
+  if (T > (int64_t(1) << 25)) return fail(DG_UNSUPPORTED, "%s: at most 2^25 tokens a call (got %lld)", fname, (long long)T);
+  if (!(scale - scale == 0.0f)) return fail(DG_INVALID_ARG, "%s: scale must be finite", fname);
+  return DG_OK;
+}
+
+// A paged cache tensor [pages, Hkv, P, D] (strides of the first three dims
+// free, rows of D bytes 16-byte aligned) and its scales [pages, Hkv].
+int check_cache(const dg_tensor* c, const char* name, const dg_tensor* sc, const char* sname, const char* fname) {
+  DG_TRY(check_basic(c, name, true));
+  DG_TRY(check_dtype(c, name, DG_E4M3));
+  DG_TRY(check_basic(sc, sname, false));
+  DG_TRY(check_dtype(sc, sname, DG_F32));
+  if (c->ndim != 4) return fail(DG_INVALID_ARG, "%s: %s must be [pages, Hkv, P, D]", fname, name);
+  if (sc->ndim != 2 || sc->shape[0] != c->shape[0] || sc->shape[1] != c->shape[1])
+    return fail(DG_INVALID_ARG, "%s: %s must be [pages, Hkv] = [%lld, %lld]", fname, sname, (long long)c->shape[0],
+                (long long)c->shape[1]);
+  if (!aligned(sc->data, 4)) return fail(DG_INVALID_ARG, "%s: %s must be 4-byte aligned", fname, sname);
+  const int64_t P = c->shape[2], D = c->shape[3];
+  if (D != 64 && D != 128 && D != 256)
+    return fail(DG_UNSUPPORTED, "%s: head size %lld is not 64, 128 or 256", fname, (long long)D);
+  if (P != 16 && P != 32 && P != 64 && P != 128)
+    return fail(DG_UNSUPPORTED, "%s: page size %lld is not 16, 32, 64 or 128", fname, (long long)P);
+  if (!aligned(c->data, 16) || c->stride[0] % 16 || c->stride[1] % 16 || c->stride[2] % 16)
+    return fail(DG_INVALID_ARG, "%s: %s needs a 16-byte aligned base and strides", fname, name);
+  if (c->stride[2] >= (int64_t(1) << 26))  // 32-bit offsets inside 16 tokens
+    return fail(DG_UNSUPPORTED, "%s: the token stride of %s must be below 2^26 bytes", fname, name);
+  return DG_OK;
+}
+
+int check_caches(const dg_tensor* kc, const dg_tensor* ks, const dg_tensor* vc, const dg_tensor* vs, const char* fname) {
+  DG_TRY(check_cache(kc, "k_cache", ks, "k_scale", fname));
+  DG_TRY(check_cache(vc, "v_cache", vs, "v_scale", fname));
+  for (int i = 0; i < 4; ++i)
+    if (kc->shape[i] != vc->shape[i]) return fail(DG_INVALID_ARG, "%s: k_cache and v_cache differ in shape", fname);
+  return DG_OK;
+}
+
+int check_table(const dg_tensor* t, int64_t S, int64_t P, const char* fname) {
+  DG_TRY(check_basic(t, "block_table", true));
+  DG_TRY(check_dtype(t, "block_table", DG_I32));
+  if (t->ndim != 2 || t->shape[0] != S)
+    return fail(DG_INVALID_ARG, "%s: block_table must be [S = %lld, max_pages]", fname, (long long)S);
+  if (t->shape[1] * P > INT32_MAX - 256)
+    return fail(DG_UNSUPPORTED, "%s: max_pages * P must be below 2^31 - 256", fname);
+  if (!aligned(t->data, 4)) return fail(DG_INVALID_ARG, "%s: block_table must be 4-byte aligned", fname);
+  return DG_OK;
+}
+
+int check_ints(const dg_tensor* t, const char* name, int64_t n, const char* fname) {
+  DG_TRY(check_basic(t, name, true));
+  DG_TRY(check_dtype(t, name, DG_I32));
+  if (t->ndim != 1 || t->shape[0] != n)
+    return fail(DG_INVALID_ARG, "%s: %s must be I32 [%lld]", fname, name, (long long)n);
+  if (!aligned(t->data, 4)) return fail(DG_INVALID_ARG, "%s: %s must be 4-byte aligned", fname, name);
+  return DG_OK;
+}
+
+// Head rows of D elements [.., D] read or written 16 bytes at a time.
+int check_heads(const dg_tensor* t, const char* name, const char* fname) {
+  const int es = elem_size(t->dtype);
+  bool ok = aligned(t->data, 16);
+  for (int i = 0; i + 1 < t->ndim; ++i) ok = ok && (t->shape[i] <= 1 || t->stride[i] * es % 16 == 0);
+  if (!ok) return fail(DG_INVALID_ARG, "%s: %s needs a 16-byte aligned base and strides", fname, name);
+  return DG_OK;
+}
+
+}  // namespace
+
+int moe_route_topk(const dg_tensor* logits, const dg_tensor* bias, const dg_tensor* topk_idx,
+                   const dg_tensor* topk_weights, int32_t score, int32_t n_group, int32_t topk_group,
+                   int32_t group_top, int renormalize, float scale, hipStream_t stream) {
+  const char* fname = "moe_route_topk";
+  DG_TRY(check_logits(logits, "logits", fname));
+  DG_TRY(check_basic(topk_idx, "topk_idx", true));
+  if (topk_idx->ndim != 2) return fail(DG_INVALID_ARG, "%s: topk_idx must be [T, k]", fname);
+  const int64_t T = logits->shape[0], E = logits->shape[1], k = topk_idx->shape[1];
+  DG_TRY(check_routes(topk_idx, "topk_idx", DG_I32, T, k, fname));
+  DG_TRY(check_routes(topk_weights, "topk_weights", DG_F32, T, k, fname));
+  if (bias != nullptr) {
+    DG_TRY(check_basic(bias, "bias", true));
+    DG_TRY(check_dtype(bias, "bias", DG_F32));
+    if (bias->ndim != 1 || bias->shape[0] != E) return fail(DG_INVALID_ARG, "%s: bias must be F32 [E = %lld]", fname, (long long)E);
+    if (!aligned(bias->data, 4)) return fail(DG_INVALID_ARG, "%s: bias must be 4-byte aligned", fname);
+  }
+  DG_TRY(check_route_limits(T, E, k, score, scale, fname));
+  if (n_group < 1 || (E > 0 && E % n_group != 0))
+    return fail(DG_INVALID_ARG, "%s: n_group = %d must divide E = %lld", fname, n_group, (long long)E);
+  if (n_group > 64) return fail(DG_UNSUPPORTED, "%s: at most 64 groups (got %d)", fname, n_group);
+  if (topk_group < 1 || topk_group > n_group)
+    return fail(DG_INVALID_ARG, "%s: topk_group must be in 1..n_group (got %d)", fname, topk_group);
+  if (group_top != 1 && group_top != 2) return fail(DG_INVALID_ARG, "%s: group_top must be 1 or 2 (got %d)", fname, group_top);
+  if (topk_group * (E / n_group) < k)
+    return fail(DG_INVALID_ARG, "%s: %d groups of %lld experts hold fewer than k = %lld", fname, topk_group,
+                (long long)(E / n_group), (long long)k);
+  DG_TRY(check_rows_apart(topk_idx, "topk_idx"));
+  DG_TRY(check_rows_apart(topk_weights, "topk_weights"));
+  DG_TRY(check_no_alias(topk_idx, "topk_idx", logits, "logits"));
+  DG_TRY(check_no_alias(topk_idx, "topk_idx", bias, "bias"));
+  DG_TRY(check_no_alias(topk_weights, "topk_weights", logits, "logits"));
+  DG_TRY(check_no_alias(topk_weights, "topk_weights", bias, "bias"));
+  DG_TRY(check_no_alias(topk_weights, "topk_weights", topk_idx, "topk_idx"));
+  if (T == 0 || k == 0) return ok();
+  dgmi::RouteTopkArgs p = {};
+  p.logits = logits->data;
+  p.sl = logits->stride[0];
+  p.bf16 = logits->dtype == DG_BF16;
+  p.bias = bias ? static_cast<const float*>(bias->data) : nullptr;
+  p.idx = static_cast<int32_t*>(topk_idx->data);
+  p.si = topk_idx->stride[0];
+  p.w = static_cast<float*>(topk_weights->data);
+  p.sw = topk_weights->stride[0];
+  p.T = (int32_t)T;
+  p.E = (int32_t)E;
+  p.k = (int32_t)k;
+  p.n_group = topk_group == n_group ? 1 : n_group;  // every group stays
+  p.group_size = (int32_t)(E / n_group);
+  p.topk_group = topk_group;
+  p.group_top = group_top;
+  p.softmax = score == DG_SCORE_SOFTMAX;
+  p.renorm = renormalize ? 1 : 0;
+  p.scale = scale;
+  return check_launch(dgmi::launch_moe_route_topk(p, stream), fname);
+}
+
+int moe_route_topk_bwd(const dg_tensor* logits, const dg_tensor* topk_idx, const dg_tensor* grad_weights,
+                       const dg_tensor* grad_logits, int32_t score, int renormalize, float scale, hipStream_t stream) {
+  const char* fname = "moe_route_topk_bwd";
+  DG_TRY(check_logits(logits, "logits", fname));
+  DG_TRY(check_logits(grad_logits, "grad_logits", fname));
+  DG_TRY(check_basic(topk_idx, "topk_idx", true));
+  if (topk_idx->ndim != 2) return fail(DG_INVALID_ARG, "%s: topk_idx must be [T, k]", fname);
+  const int64_t T = logits->shape[0], E = logits->shape[1], k = topk_idx->shape[1];
+  if (grad_logits->shape[0] != T || grad_logits->shape[1] != E)
+    return fail(DG_INVALID_ARG, "%s: grad_logits must have the shape of logits", fname);
+  DG_TRY(check_routes(topk_idx, "topk_idx", DG_I32, T, k, fname));
+  DG_TRY(check_routes(grad_weights, "grad_weights", DG_F32, T, k, fname));
+  DG_TRY(check_route_limits(T, E, k, score, scale, fname));
+  DG_TRY(check_rows_apart(grad_logits, "grad_logits"));
+  DG_TRY(check_no_alias(grad_logits, "grad_logits", logits, "logits"));
+  DG_TRY(check_no_alias(grad_logits, "grad_logits", topk_idx, "topk_idx"));
+  DG_TRY(check_no_alias(grad_logits, "grad_logits", grad_weights, "grad_weights"));
+  if (T == 0 || E == 0) return ok();
+  dgmi::RouteTopkBwdArgs p = {};
+  p.logits = logits->data;
+  p.sl = logits->stride[0];
+  p.bf16 = logits->dtype == DG_BF16;
+  p.idx = static_cast<const int32_t*>(topk_idx->data);
+  p.si = topk_idx->stride[0];
+  p.g = static_cast<const float*>(grad_weights->data);
+  p.sg = grad_weights->stride[0];
+  p.dlogits = grad_logits->data;
+  p.so = grad_logits->stride[0];
+  p.out_bf16 = grad_logits->dtype == DG_BF16;
+  p.T = (int32_t)T;
+  p.E = (int32_t)E;
+  p.k = (int32_t)k;
+  p.softmax = score == DG_SCORE_SOFTMAX;
+  p.renorm = renormalize ? 1 : 0;
+  p.scale = scale;
+  return check_launch(dgmi::launch_moe_route_topk_bwd(p, stream), fname);
+}
+
+int kv_append_fp8(const dg_tensor* k, const dg_tensor* v, const dg_tensor* k_cache, const dg_tensor* v_cache,
+                  const dg_tensor* k_scale, const dg_tensor* v_scale, const dg_tensor* block_table,
+                  const dg_tensor* cu_tokens, const dg_tensor* start, const dg_tensor* cos_sin, const dg_tensor* q,
+                  const dg_tensor* q_out, int interleaved, hipStream_t stream) {
+  const char* fname = "kv_append_fp8";
+  DG_TRY(check_basic(k, "k", true));
+  DG_TRY(check_basic(v, "v", true));
+  if (k->dtype != DG_F32 && k->dtype != DG_BF16) return fail(DG_INVALID_ARG, "%s: k must be F32 or BF16", fname);
+  DG_TRY(check_dtype(v, "v", k->dtype));
+  DG_TRY(check_caches(k_cache, k_scale, v_cache, v_scale, fname));
+  const int64_t pages = k_cache->shape[0], Hkv = k_cache->shape[1], P = k_cache->shape[2], D = k_cache->shape[3];
+  if (k->ndim != 3 || v->ndim != 3) return fail(DG_INVALID_ARG, "%s: k and v must be [T, Hkv, D]", fname);
+  const int64_t T = k->shape[0];
+  for (const dg_tensor* t : {k, v})
+    if (t->shape[0] != T || t->shape[1] != Hkv || t->shape[2] != D)
+      return fail(DG_INVALID_ARG, "%s: k and v must be [T, Hkv, D] = [%lld, %lld, %lld]", fname, (long long)T,
+                  (long long)Hkv, (long long)D);
+  DG_TRY(check_heads(k, "k", fname));
+  DG_TRY(check_heads(v, "v", fname));
+  DG_TRY(check_basic(start, "start", true));
+  if (start->ndim != 1) return fail(DG_INVALID_ARG, "%s: start must be [S]", fname);
+  const int64_t S = start->shape[0];
+  DG_TRY(check_ints(start, "start", S, fname));
+  DG_TRY(check_ints(cu_tokens, "cu_tokens", S + 1, fname));
+  DG_TRY(check_table(block_table, S, P, fname));
+  int64_t rot = 0;
+  if (cos_sin != nullptr) {
+    DG_TRY(check_basic(cos_sin, "cos_sin", true));
+    DG_TRY(check_dtype(cos_sin, "cos_sin", DG_F32));
+    if (cos_sin->ndim != 2) return fail(DG_INVALID_ARG, "%s: cos_sin must be [positions, rot]", fname);
+    rot = cos_sin->shape[1];
+    if (rot > D || rot % 16 != 0)
+      return fail(DG_INVALID_ARG, "%s: rot = %lld must be a multiple of 16, at most D = %lld", fname, (long long)rot, (long long)D);
+    DG_TRY(check_heads(cos_sin, "cos_sin", fname));
+  }
+  if ((q == nullptr) != (q_out == nullptr)) return fail(DG_INVALID_ARG, "%s: q and q_out go together", fname);
+  int64_t Hq = 0;
+  if (q != nullptr) {
+    DG_TRY(check_basic(q, "q", true));
+    DG_TRY(check_basic(q_out, "q_out", true));
+    DG_TRY(check_dtype(q, "q", k->dtype));
+    DG_TRY(check_dtype(q_out, "q_out", DG_BF16));
+    if (q->ndim != 3 || q_out->ndim != 3 || q->shape[0] != T || q->shape[2] != D || q_out->shape[0] != T ||
+        q_out->shape[1] != q->shape[1] || q_out->shape[2] != D)
+      return fail(DG_INVALID_ARG, "%s: q and q_out must be [T, Hq, D] with T = %lld, D = %lld", fname, (long long)T,
+                  (long long)D);
+    Hq = q->shape[1];
+    DG_TRY(check_heads(q, "q", fname));
+    DG_TRY(check_heads(q_out, "q_out", fname));
+    DG_TRY(check_rows_apart(q_out, "q_out"));
+  }
+  const dg_tensor* outs[] = {k_cache, v_cache, k_scale, v_scale, q_out};
+  const char* onames[] = {"k_cache", "v_cache", "k_scale", "v_scale", "q_out"};
+  const dg_tensor* ins[] = {k, v, q, block_table, cu_tokens, start, cos_sin};
+  const char* inames[] = {"k", "v", "q", "block_table", "cu_tokens", "start", "cos_sin"};
+  for (int i = 0; i < 5; ++i) {
+    if (outs[i] == nullptr) continue;
+    for (int j = 0; j < 7; ++j) DG_TRY(check_no_alias(outs[i], onames[i], ins[j], inames[j]));
+    for (int j = i + 1; j < 5; ++j) {
+      if (i % 2 == 0 && i < 4 && j == i + 1) continue;  // K and V of one pool may be interleaved (below)
+      DG_TRY(check_no_alias(outs[i], onames[i], outs[j], onames[j]));
+    }
+    DG_TRY(check_rows_apart(outs[i], onames[i]));
+  }
+  // k_cache and v_cache (and their scales) may be the two halves of one pool,
+  // page by page or head by head, but not the same memory
+  if (pages > 0 && (k_cache->data == v_cache->data || k_scale->data == v_scale->data))
+    return fail(DG_INVALID_ARG, "%s: v_cache and v_scale must not be k_cache and k_scale", fname);
+  if (T == 0 || S == 0 || pages == 0 || Hkv == 0) {
+    if (q == nullptr || T == 0 || S == 0 || Hq == 0) return ok();
+  }
+  dgmi::KvAppendArgs p = {};
+  p.k = k->data;
+  p.v = v->data;
+  p.q = Hq > 0 ? q->data : nullptr;
+  p.bf16 = k->dtype == DG_BF16;
+  p.sk_t = k->stride[0];
+  p.sk_h = k->stride[1];
+  p.sv_t = v->stride[0];
+  p.sv_h = v->stride[1];
+  if (q != nullptr) {
+    p.sq_t = q->stride[0];
+    p.sq_h = q->stride[1];
+    p.q_out = static_cast<uint16_t*>(q_out->data);
+    p.so_t = q_out->stride[0];
+    p.so_h = q_out->stride[1];
+  }
+  if (cos_sin != nullptr) {
+    p.cos_sin = static_cast<const float*>(cos_sin->data);
+    p.s_cs = cos_sin->stride[0];
+    p.positions = cos_sin->shape[0];
+  }
+  p.rot = (int32_t)rot;
+  p.interleaved = interleaved ? 1 : 0;
+  p.k_cache = static_cast<uint8_t*>(k_cache->data);
+  p.v_cache = static_cast<uint8_t*>(v_cache->data);
+  p.skc_p = k_cache->stride[0];
+  p.skc_h = k_cache->stride[1];
+  p.skc_t = k_cache->stride[2];
+  p.svc_p = v_cache->stride[0];
+  p.svc_h = v_cache->stride[1];
+  p.svc_t = v_cache->stride[2];
+  p.k_scale = static_cast<float*>(k_scale->data);
+  p.v_scale = static_cast<float*>(v_scale->data);
+  p.sks_p = k_scale->stride[0];
+  p.sks_h = k_scale->stride[1];
+  p.svs_p = v_scale->stride[0];
+  p.svs_h = v_scale->stride[1];
+  p.table = static_cast<const int32_t*>(block_table->data);
+  p.s_table = block_table->stride[0];
+  p.max_pages = (int32_t)block_table->shape[1];
+  p.pages = (int32_t)pages;
+  p.cu = static_cast<const int32_t*>(cu_tokens->data);
+  p.start = static_cast<const int32_t*>(start->data);
+  p.T = (int32_t)T;
+  p.S = (int32_t)S;
+  p.Hkv = (int32_t)Hkv;
+  p.Hq = (int32_t)Hq;
+  p.D = (int32_t)D;
+  p.P = (int32_t)P;
+  int64_t kv_blocks;
+  int by_token;
+  if (dgmi::kv_append_grid(T, S, P, Hkv, p.q != nullptr, &kv_blocks, &by_token) > kMaxGroups)
+    return fail(DG_UNSUPPORTED, "%s: too many tokens times heads for one launch", fname);
+  return check_launch(dgmi::launch_kv_append(p, stream), fname);
+}
+
+int64_t paged_attention_fp8_workspace(int64_t S, int64_t n, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_tokens) {
+  if (S <= 0 || n <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || max_tokens <= 0) return 0;
+  return dgmi::paged_attention_workspace(S, n, Hq, Hkv, D, max_tokens);
+}
+
+int paged_attention_fp8(const dg_tensor* q, const dg_tensor* k_cache, const dg_tensor* v_cache,
+                        const dg_tensor* k_scale, const dg_tensor* v_scale, const dg_tensor* block_table,
+                        const dg_tensor* seq_lens, const dg_tensor* out, const dg_tensor* lse,
+                        const dg_tensor* workspace, float scale, int32_t window, hipStream_t stream) {
+  const char* fname = "paged_attention_fp8";
+  DG_TRY(check_basic(q, "q", true));
+  DG_TRY(check_basic(out, "out", true));
+  DG_TRY(check_dtype(q, "q", DG_BF16));
+  DG_TRY(check_dtype(out, "out", DG_BF16));
+  DG_TRY(check_caches(k_cache, k_scale, v_cache, v_scale, fname));
+  const int64_t pages = k_cache->shape[0], Hkv = k_cache->shape[1], P = k_cache->shape[2], D = k_cache->shape[3];
+  if (q->ndim != 4 || q->shape[3] != D) return fail(DG_INVALID_ARG, "%s: q must be [S, n, Hq, D = %lld]", fname, (long long)D);
+  const int64_t S = q->shape[0], n = q->shape[1], Hq = q->shape[2];
+  if (out->ndim != 4 || out->shape[0] != S || out->shape[1] != n || out->shape[2] != Hq || out->shape[3] != D)
+    return fail(DG_INVALID_ARG, "%s: out must have the shape of q", fname);
+  if (Hkv == 0 ? Hq != 0 : Hq % Hkv != 0)
+    return fail(DG_INVALID_ARG, "%s: Hq = %lld is not a multiple of Hkv = %lld", fname, (long long)Hq, (long long)Hkv);
+  DG_TRY(check_heads(q, "q", fname));
+  DG_TRY(check_heads(out, "out", fname));
+  DG_TRY(check_rows_apart(out, "out"));
+  DG_TRY(check_ints(seq_lens, "seq_lens", S, fname));
+  DG_TRY(check_table(block_table, S, P, fname));
+  if (window < 0) return fail(DG_INVALID_ARG, "%s: window must be >= 0 (got %d)", fname, window);
+  if (!(scale - scale == 0.0f)) return fail(DG_INVALID_ARG, "%s: scale must be finite", fname);
+  if (lse != nullptr) {
+    DG_TRY(check_basic(lse, "lse", false));
+    DG_TRY(check_dtype(lse, "lse", DG_F32));
+    if (lse->ndim != 3 || lse->shape[0] != S || lse->shape[1] != n || lse->shape[2] != Hq)
+      return fail(DG_INVALID_ARG, "%s: lse must be [S, n, Hq]", fname);
+    if (!aligned(lse->data, 4)) return fail(DG_INVALID_ARG, "%s: lse must be 4-byte aligned", fname);
+    DG_TRY(check_rows_apart(lse, "lse"));
+  }
+  const int64_t group = Hkv > 0 ? Hq / Hkv : 0, rows = n * group, row_tiles = (rows + 15) / 16;
+  if (rows > INT32_MAX - 16 || S * Hkv * row_tiles > kMaxGroups)
+    return fail(DG_UNSUPPORTED, "%s: too many queries for one launch", fname);
+  const int64_t need = paged_attention_fp8_workspace(S, n, Hq, Hkv, D, block_table->shape[1] * P);
+  if (need > 0) {
+    if (workspace == nullptr) return fail(DG_INVALID_ARG, "%s: workspace of %lld bytes needed", fname, (long long)need);
+    DG_TRY(check_basic(workspace, "workspace", true));
+    DG_TRY(check_dtype(workspace, "workspace", DG_F32));
+    if (workspace->ndim != 1 || workspace->shape[0] * 4 < need)
+      return fail(DG_INVALID_ARG, "%s: workspace must be F32 [at least %lld]", fname, (long long)((need + 3) / 4));
+    if (!aligned(workspace->data, 16)) return fail(DG_INVALID_ARG, "%s: workspace must be 16-byte aligned", fname);
+  }
+  const dg_tensor* outs[] = {out, lse, need > 0 ? workspace : nullptr};
+  const char* onames[] = {"out", "lse", "workspace"};
+  const dg_tensor* ins[] = {q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens};
+  const char* inames[] = {"q", "k_cache", "v_cache", "k_scale", "v_scale", "block_table", "seq_lens"};
+  for (int i = 0; i < 3; ++i) {
+    if (outs[i] == nullptr) continue;
+    for (int j = 0; j < 7; ++j) DG_TRY(check_no_alias(outs[i], onames[i], ins[j], inames[j]));
+    for (int j = i + 1; j < 3; ++j) DG_TRY(check_no_alias(outs[i], onames[i], outs[j], onames[j]));
+  }
+  if (S == 0 || rows == 0) return ok();
+  dgmi::PagedAttnArgs p = {};
+  p.q = static_cast<const uint16_t*>(q->data);
+  p.sq_s = q->stride[0];
+  p.sq_n = q->stride[1];
+  p.sq_h = q->stride[2];
+  p.out = static_cast<uint16_t*>(out->data);
+  p.so_s = out->stride[0];
+  p.so_n = out->stride[1];
+  p.so_h = out->stride[2];
+  if (lse != nullptr) {
+    p.lse = static_cast<float*>(lse->data);
+    p.sl_s = lse->stride[0];
+    p.sl_n = lse->stride[1];
+    p.sl_h = lse->stride[2];
+  }
+  p.k_cache = static_cast<const uint8_t*>(k_cache->data);
+  p.v_cache = static_cast<const uint8_t*>(v_cache->data);
+  p.skc_p = k_cache->stride[0];
+  p.skc_h = k_cache->stride[1];
+  p.skc_t = k_cache->stride[2];
+  p.svc_p = v_cache->stride[0];
+  p.svc_h = v_cache->stride[1];
+  p.svc_t = v_cache->stride[2];
+  p.k_scale = static_cast<const float*>(k_scale->data);
+  p.v_scale = static_cast<const float*>(v_scale->data);
+  p.sks_p = k_scale->stride[0];
+  p.sks_h = k_scale->stride[1];
+  p.svs_p = v_scale->stride[0];
+  p.svs_h = v_scale->stride[1];
+  p.table = static_cast<const int32_t*>(block_table->data);
+  p.s_table = block_table->stride[0];
+  p.lens = static_cast<const int32_t*>(seq_lens->data);
+  p.S = (int32_t)S;
+  p.n = (int32_t)n;
+  p.Hkv = (int32_t)Hkv;
+  p.group = (int32_t)group;
+  p.rows = (int32_t)rows;
+  p.row_tiles = (int32_t)row_tiles;
+  p.D = (int32_t)D;
+  p.P = (int32_t)P;
+  p.max_pages = (int32_t)block_table->shape[1];
+  p.pages = (int32_t)pages;
+  p.window = window;
+  p.scale = scale;
+  p.workspace = need > 0 ? static_cast<float*>(workspace->data) : nullptr;
+  return check_launch(dgmi::launch_paged_attention(p, stream), fname);
+}
+
 int dg_query_config(int32_t kind, int64_t G, int64_t M, int64_t N, int64_t K, dg_config* out) {
   if (out == nullptr) return fail(DG_INVALID_ARG, "dg_query_config: out is NULL");
   if (G < 0 || M < 0 || N < 0 || K < 0) return fail(DG_INVALID_ARG, "dg_query_config: negative size");

@@ -74,6 +74,86 @@ struct MoeCombineArgs {
   int32_t col_blocks;  // set by the launcher
 };
 
+// Expert routing (route.hip): logits [T, E] (row stride sl, FP32 or BF16),
+// bias [E] or NULL, idx and w [T, k] (row strides si, sw).
+struct RouteTopkArgs {
+  const void* logits;
+  int64_t sl;
+  int32_t bf16;
+  const float* bias;
+  int32_t* idx;
+  int64_t si;
+  float* w;
+  int64_t sw;
+  int32_t T, E, k;
+  int32_t n_group, group_size, topk_group, group_top;
+  int32_t softmax, renorm;
+  float scale;
+};
+
+struct RouteTopkBwdArgs {
+  const void* logits;
+  int64_t sl;
+  int32_t bf16;
+  const int32_t* idx;
+  int64_t si;
+  const float* g;
+  int64_t sg;
+  void* dlogits;
+  int64_t so;
+  int32_t out_bf16;
+  int32_t T, E, k;
+  int32_t softmax, renorm;
+  float scale;
+};
+
+// Append to the paged FP8 cache (kvcache.hip): k, v [T, Hkv, D], q and q_out
+// [T, Hq, D], caches [pages, Hkv, P, D], scales [pages, Hkv], table
+// [S, max_pages], cu [S + 1], start [S], cos_sin [positions, rot].
+struct KvAppendArgs {
+  const void *k, *v, *q;
+  int32_t bf16;
+  int64_t sk_t, sk_h, sv_t, sv_h, sq_t, sq_h;
+  uint16_t* q_out;
+  int64_t so_t, so_h;
+  const float* cos_sin;
+  int64_t s_cs;
+  int32_t rot, interleaved;
+  int64_t positions;
+  uint8_t *k_cache, *v_cache;
+  int64_t skc_p, skc_h, skc_t, svc_p, svc_h, svc_t;
+  float *k_scale, *v_scale;
+  int64_t sks_p, sks_h, svs_p, svs_h;
+  const int32_t* table;
+  int64_t s_table;
+  int32_t max_pages, pages;
+  const int32_t *cu, *start;
+  int32_t T, S, Hkv, Hq, D, P;
+  int64_t kv_blocks;  // set by the launcher
+  int32_t by_token;   // set by the launcher
+};
+
+// Attention over the paged FP8 cache (attn.hip): q and out [S, n, Hq, D],
+// lse [S, n, Hq] or NULL; rows = n * group, row_tiles = ceil(rows / 16).
+struct PagedAttnArgs {
+  const uint16_t* q;
+  int64_t sq_s, sq_n, sq_h;
+  uint16_t* out;
+  int64_t so_s, so_n, so_h;
+  float* lse;
+  int64_t sl_s, sl_n, sl_h;
+  const uint8_t *k_cache, *v_cache;
+  int64_t skc_p, skc_h, skc_t, svc_p, svc_h, svc_t;
+  const float *k_scale, *v_scale;
+  int64_t sks_p, sks_h, svs_p, svs_h;
+  const int32_t* table;
+  int64_t s_table;
+  const int32_t* lens;
+  int32_t S, n, Hkv, group, rows, row_tiles, D, P, max_pages, pages, window;
+  float scale;
+  float* workspace;
+};
+
 struct PackArgs {
   const float* x;
   int64_t sx_g, sx_r;
@@ -95,6 +175,12 @@ hipError_t launch_cast_mn(const QuantTArgs& p, bool per_block, hipStream_t strea
 hipError_t launch_moe_route(const MoeRouteArgs& p, hipStream_t stream);
 hipError_t launch_moe_route_contiguous(const MoeRouteArgs& p, hipStream_t stream);
 hipError_t launch_moe_combine(const MoeCombineArgs& p, hipStream_t stream);
+hipError_t launch_moe_route_topk(const RouteTopkArgs& p, hipStream_t stream);
+hipError_t launch_moe_route_topk_bwd(const RouteTopkBwdArgs& p, hipStream_t stream);
+int64_t kv_append_grid(int64_t T, int64_t S, int64_t P, int64_t Hkv, bool q, int64_t* kv_blocks, int* by_token);
+hipError_t launch_kv_append(KvAppendArgs p, hipStream_t stream);
+int64_t paged_attention_workspace(int64_t S, int64_t n, int64_t Hq, int64_t Hkv, int64_t D, int64_t cap);
+hipError_t launch_paged_attention(const PagedAttnArgs& p, hipStream_t stream);
 hipError_t launch_per_block(const QuantArgs& p, hipStream_t stream);
 hipError_t launch_pack_ue8m0(const PackArgs& p, hipStream_t stream);
 

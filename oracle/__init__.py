@@ -19,6 +19,9 @@ Modules
   moe      -- the steps either side of the masked grouped GEMM: routing of
               (token, choice) pairs into expert buffers with the per-token
               cast, and the weighted combine of the GEMM's rows per token.
+  router   -- expert routing (scores, groups, top-k, weights) and its gradient.
+  attention -- the paged FP8 key/value cache: append with the position
+             rotation, attention over it.
 
 Sources (the pages this follows):
   * "DeepInside DeepGEMM: Unpacking DeepSeek's Unified Tensor Core Library
