@@ -1335,6 +1335,8 @@ int paged_attention_fp8(const dg_tensor* q, const dg_tensor* k_cache, const dg_t
   const int64_t group = Hkv > 0 ? Hq / Hkv : 0, rows = n * group, row_tiles = (rows + 15) / 16;
   if (rows > INT32_MAX - 16 || S * Hkv * row_tiles > kMaxGroups)
     return fail(DG_UNSUPPORTED, "%s: too many queries for one launch", fname);
+  if (Hkv * row_tiles * (block_table->shape[1] * P / 32 + 1) > INT32_MAX)
+    return fail(DG_UNSUPPORTED, "%s: too many tokens times heads for one sequence", fname);
   const int64_t need = paged_attention_fp8_workspace(S, n, Hq, Hkv, D, block_table->shape[1] * P);
   if (need > 0) {
     if (workspace == nullptr) return fail(DG_INVALID_ARG, "%s: workspace of %lld bytes needed", fname, (long long)need);
