@@ -1333,7 +1333,8 @@ int paged_attention_fp8(const dg_tensor* q, const dg_tensor* k_cache, const dg_t
     DG_TRY(check_rows_apart(lse, "lse"));
   }
   const int64_t group = Hkv > 0 ? Hq / Hkv : 0, rows = n * group, row_tiles = (rows + 15) / 16;
-  if (rows > INT32_MAX - 16 || S * Hkv * row_tiles > kMaxGroups)
+  if (rows > INT32_MAX - 16 || Hkv * row_tiles > INT32_MAX ||
+      (row_tiles > 0 && dgmi::paged_attention_grid(S, Hkv, row_tiles, D, block_table->shape[1] * P) > kMaxGroups))
     return fail(DG_UNSUPPORTED, "%s: too many queries for one launch", fname);
   if (Hkv * row_tiles * (block_table->shape[1] * P / 32 + 1) > INT32_MAX)
     return fail(DG_UNSUPPORTED, "%s: too many tokens times heads for one sequence", fname);

@@ -152,10 +152,10 @@ struct PagedAttnArgs {
   int32_t S, n, Hkv, group, rows, row_tiles, D, P, max_pages, pages, window;
   float scale;
   float* workspace;
-  // set by the launcher: units (KV head, row tile) per sequence, workgroups of
-  // the first kernel, tiles a workgroup takes at least, workgroups per unit of
-  // the join, log2 P
-  int32_t units, shares, min_share, slices, log_p;
+  // set by the launcher: row tiles a workgroup takes together, units (KV head,
+  // group of row tiles) per sequence, groups per head, workgroups of the first kernel, tiles a
+  // workgroup takes at least, rows per workgroup of the join, log2 P
+  int32_t rt, units, groups, shares, min_share, rps, log_p;
 };
 
 struct PackArgs {
@@ -184,6 +184,8 @@ hipError_t launch_moe_route_topk_bwd(const RouteTopkBwdArgs& p, hipStream_t stre
 int64_t kv_append_grid(int64_t T, int64_t S, int64_t P, int64_t Hkv, bool q, int64_t* kv_blocks, int* by_token);
 hipError_t launch_kv_append(KvAppendArgs p, hipStream_t stream);
 int64_t paged_attention_workspace(int64_t S, int64_t n, int64_t Hq, int64_t Hkv, int64_t D, int64_t cap);
+// largest grid of the call's kernels
+int64_t paged_attention_grid(int64_t S, int64_t Hkv, int64_t row_tiles, int64_t D, int64_t cap);
 hipError_t launch_paged_attention(PagedAttnArgs p, hipStream_t stream);
 hipError_t launch_per_block(const QuantArgs& p, hipStream_t stream);
 hipError_t launch_pack_ue8m0(const PackArgs& p, hipStream_t stream);
