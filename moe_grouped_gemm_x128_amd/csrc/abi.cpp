@@ -1121,7 +1121,7 @@ int moe_route_topk(const dg_tensor* logits, const dg_tensor* bias, const dg_tens
   p.E = (int32_t)E;
   p.k = (int32_t)k;
   p.n_group = topk_group == n_group ? 1 : n_group;  // every group stays
-  p.group_size = (int32_t)(E / n_group);
+  p.group_size = (int32_t)(E / p.n_group);
   p.topk_group = topk_group;
   p.group_top = group_top;
   p.softmax = score == DG_SCORE_SOFTMAX;

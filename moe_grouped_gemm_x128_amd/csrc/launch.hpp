@@ -89,6 +89,8 @@ struct RouteTopkArgs {
   int32_t n_group, group_size, topk_group, group_top;
   int32_t softmax, renorm;
   float scale;
+  // set by the launcher: log2 of a group's lanes, 16-byte loads
+  int32_t log_l, vec, vec_bias;
 };
 
 struct RouteTopkBwdArgs {
@@ -105,6 +107,7 @@ struct RouteTopkBwdArgs {
   int32_t T, E, k;
   int32_t softmax, renorm;
   float scale;
+  int32_t vec, vec_out;  // set by the launcher
 };
 
 // Append to the paged FP8 cache (kvcache.hip): k, v [T, Hkv, D], q and q_out
@@ -179,8 +182,8 @@ hipError_t launch_cast_mn(const QuantTArgs& p, bool per_block, hipStream_t strea
 hipError_t launch_moe_route(const MoeRouteArgs& p, hipStream_t stream);
 hipError_t launch_moe_route_contiguous(const MoeRouteArgs& p, hipStream_t stream);
 hipError_t launch_moe_combine(const MoeCombineArgs& p, hipStream_t stream);
-hipError_t launch_moe_route_topk(const RouteTopkArgs& p, hipStream_t stream);
-hipError_t launch_moe_route_topk_bwd(const RouteTopkBwdArgs& p, hipStream_t stream);
+hipError_t launch_moe_route_topk(RouteTopkArgs p, hipStream_t stream);
+hipError_t launch_moe_route_topk_bwd(RouteTopkBwdArgs p, hipStream_t stream);
 int64_t kv_append_grid(int64_t T, int64_t S, int64_t P, int64_t Hkv, bool q, int64_t* kv_blocks, int* by_token);
 hipError_t launch_kv_append(KvAppendArgs p, hipStream_t stream);
 int64_t paged_attention_workspace(int64_t S, int64_t n, int64_t Hq, int64_t Hkv, int64_t D, int64_t cap);

@@ -121,6 +121,32 @@ def test_route_matches_oracle(T, E, k, score, bias, groups, renorm, scale, bf16)
     _check(xv, k, idx, w, b, kw, f"T={T} E={E}")
 
 
+@pytest.mark.parametrize("T,E,k,score,bias,groups,renorm,bf16", [
+    (2049, 96, 5, "sigmoid", True, (8, 3, 2), True, False),
+    (2500, 400, 8, "softmax", False, (1, 1, 1), False, True),
+    (3000, 30, 20, "sigmoid", False, (30, 25, 1), True, False),    # groups of one, more choices than 16 lanes
+    (2100, 128, 40, "softmax", False, (1, 1, 1), True, False),     # more than 32
+    (8193, 64, 6, "softmax", False, (8, 3, 1), False, True),
+    (8200, 256, 8, "sigmoid", True, (8, 4, 2), True, False),
+    (8205, 93, 3, "sigmoid", False, (3, 2, 2), True, True),        # groups of 31 on four lanes each
+    (8300, 20, 18, "softmax", False, (1, 1, 1), True, False),
+    (8193, 1, 1, "sigmoid", False, (1, 1, 1), False, False),
+])
+def test_many_tokens(T, E, k, score, bias, groups, renorm, bf16):
+    """Token counts at which a token takes fewer lanes; ties included."""
+    say(f"moe_route_topk many tokens T={T} E={E} k={k} {score} groups={groups}")
+    rng = np.random.default_rng(900 + E)
+    x = rng.normal(size=(T, E)).astype(np.float32) * 2
+    x[5:40] = np.round(x[5:40])      # ties
+    x[T - 7:T - 2] = -np.inf
+    x[T - 1, E // 2:] = -np.inf
+    b = (rng.normal(size=E) * 0.05).astype(np.float32) if bias else None
+    d, xv = _logits(x, bf16, pad=8)
+    kw = dict(score=score, n_group=groups[0], topk_group=groups[1], group_top=groups[2], renormalize=renorm)
+    idx, w = _route(d, k, bias=None if b is None else to_dev(b), **kw)
+    _check(xv, k, idx, w, b, kw, f"T={T} E={E}")
+
+
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("E,groups", [(64, (1, 1, 1)), (256, (8, 3, 2)), (96, (8, 4, 1))])
 def test_ties_go_to_the_lowest_index(score, E, groups):
@@ -202,6 +228,10 @@ def test_rows_keep_their_places():
     (17, 1024, 64, "softmax", False, False, False),
     (17, 513, 7, "sigmoid", True, False, True),
     (5, 1, 1, "softmax", True, False, False),
+    (33, 40, 20, "sigmoid", True, False, False),
+    (20, 60, 40, "softmax", False, True, False),
+    (130, 30, 18, "softmax", True, False, True),
+    (70, 200, 12, "softmax", False, False, False),
 ])
 def test_gradient_matches_oracle(T, E, k, score, renorm, bf16, out_bf16):
     say(f"moe_route_topk_bwd T={T} E={E} k={k} {score} renorm={renorm} bf16={bf16}/{out_bf16}")
