@@ -98,8 +98,8 @@ def load_library(path=None):
     if not os.path.exists(p):
         raise RuntimeError(f"libdgmi.so not found at {p}: build it with `python -m moe_grouped_gemm_x128_amd.build`")
     lib = ctypes.CDLL(p)
-    T = ctypes.POINTER(DgTensor)
     vp, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+    T = vp  # const dg_tensor*: packed bytes or a reference to a DgTensor
     sig = {
         "dg_last_error": ([], ctypes.c_char_p),
         "dgmi_init": ([], ctypes.c_int),
@@ -167,23 +167,26 @@ _PAD = ((), (0, 0, 0), (0, 0), (0,), ())
 assert _PACK.size == ctypes.sizeof(DgTensor)
 
 
-def describe(t, dtype=None):
-    """dg_tensor for a torch tensor (None -> NULL descriptor)."""
-    if t is None:
-        return None
+def _packed(t, dtype=None):
+    """A torch tensor's dg_tensor as bytes.  (Packed in one go: a call passes up
+    to a dozen tensors, and setting the structure's fields takes 4 us each.)"""
     shape = t.shape
     n = len(shape)
     if n < 1 or n > 4:
         raise ValueError("dg_tensor supports 1 to 4 dims")
     code = _dtype_code(t) if dtype is None else dtype
     pad = _PAD[n]
-    # (packed in one go: a call describes up to a dozen tensors, and setting the
-    # structure's fields one by one takes 4 us each)
-    return DgTensor.from_buffer_copy(_PACK.pack(t.data_ptr(), code, n, *shape, *pad, *t.stride(), *pad))
+    return _PACK.pack(t.data_ptr(), code, n, *shape, *pad, *t.stride(), *pad)
 
 
-def _ref(d):
-    return ctypes.byref(d) if d is not None else None
+def describe(t, dtype=None):
+    """dg_tensor for a torch tensor (None -> NULL descriptor)."""
+    return None if t is None else DgTensor.from_buffer_copy(_packed(t, dtype))
+
+
+def _arg(t):
+    """The descriptor argument of a call: the packed bytes themselves, or NULL."""
+    return None if t is None else _packed(t)
 
 
 def _stream(stream):
@@ -213,15 +216,15 @@ def dgmi_init():
 def fp8_gemm_nt(a, b, sfa, sfb, c, d, stream=None):
     """d = c + a . b^T with block scales; c is None or a BF16/F32 [M, N] tensor (may be d)."""
     lib = load_library()
-    _check(lib.fp8_gemm_nt(_ref(describe(a)), _ref(describe(b)), _ref(describe(sfa)), _ref(describe(sfb)),
-                           _ref(describe(c)), _ref(describe(d)), _stream(stream)))
+    _check(lib.fp8_gemm_nt(_arg(a), _arg(b), _arg(sfa), _arg(sfb),
+                           _arg(c), _arg(d), _stream(stream)))
     return d
 
 
 def _fp8_gemm_layout(name, a, b, sfa, sfb, c, d, stream):
     lib = load_library()
-    _check(getattr(lib, name)(_ref(describe(a)), _ref(describe(b)), _ref(describe(sfa)), _ref(describe(sfb)),
-                              _ref(describe(c)), _ref(describe(d)), _stream(stream)))
+    _check(getattr(lib, name)(_arg(a), _arg(b), _arg(sfa), _arg(sfb),
+                              _arg(c), _arg(d), _stream(stream)))
     return d
 
 
@@ -243,8 +246,8 @@ def fp8_gemm_tt(a, b, sfa, sfb, c, d, stream=None):
 def fp8_gemm_nt_fp8_out(a, b, sfa, sfb, c, q, sfq, use_ue8m0=False, stream=None):
     """(q, sfq) = per-token FP8 cast of the BF16 D = c + a . b^T, in one kernel."""
     lib = load_library()
-    _check(lib.fp8_gemm_nt_fp8_out(_ref(describe(a)), _ref(describe(b)), _ref(describe(sfa)), _ref(describe(sfb)),
-                                   _ref(describe(c)), _ref(describe(q)), _ref(describe(sfq)), int(bool(use_ue8m0)),
+    _check(lib.fp8_gemm_nt_fp8_out(_arg(a), _arg(b), _arg(sfa), _arg(sfb),
+                                   _arg(c), _arg(q), _arg(sfq), int(bool(use_ue8m0)),
                                    _stream(stream)))
     return q, sfq
 
@@ -254,13 +257,13 @@ def m_grouped_fp8_gemm_nt_contiguous(a, b, sfa, sfb, d, grouped_layout, stream=N
     accumulate form d = c + a . b^T (m_grouped_fp8_gemm_nt_contiguous_acc)."""
     lib = load_library()
     if c is not None:
-        _check(lib.m_grouped_fp8_gemm_nt_contiguous_acc(_ref(describe(a)), _ref(describe(b)), _ref(describe(sfa)),
-                                                        _ref(describe(sfb)), _ref(describe(c)), _ref(describe(d)),
-                                                        _ref(describe(grouped_layout)), _stream(stream)))
+        _check(lib.m_grouped_fp8_gemm_nt_contiguous_acc(_arg(a), _arg(b), _arg(sfa),
+                                                        _arg(sfb), _arg(c), _arg(d),
+                                                        _arg(grouped_layout), _stream(stream)))
         return d
-    _check(lib.m_grouped_fp8_gemm_nt_contiguous(_ref(describe(a)), _ref(describe(b)), _ref(describe(sfa)),
-                                                _ref(describe(sfb)), _ref(describe(d)),
-                                                _ref(describe(grouped_layout)), _stream(stream)))
+    _check(lib.m_grouped_fp8_gemm_nt_contiguous(_arg(a), _arg(b), _arg(sfa),
+                                                _arg(sfb), _arg(d),
+                                                _arg(grouped_layout), _stream(stream)))
     return d
 
 
@@ -269,12 +272,12 @@ def m_grouped_fp8_gemm_nt_masked(a, b, sfa, sfb, d, masked_m, max_m_per_group, s
     accumulate form d = c + a . b^T (m_grouped_fp8_gemm_nt_masked_acc)."""
     lib = load_library()
     if c is not None:
-        _check(lib.m_grouped_fp8_gemm_nt_masked_acc(_ref(describe(a)), _ref(describe(b)), _ref(describe(sfa)),
-                                                    _ref(describe(sfb)), _ref(describe(c)), _ref(describe(d)),
-                                                    _ref(describe(masked_m)), int(max_m_per_group), _stream(stream)))
+        _check(lib.m_grouped_fp8_gemm_nt_masked_acc(_arg(a), _arg(b), _arg(sfa),
+                                                    _arg(sfb), _arg(c), _arg(d),
+                                                    _arg(masked_m), int(max_m_per_group), _stream(stream)))
         return d
-    _check(lib.m_grouped_fp8_gemm_nt_masked(_ref(describe(a)), _ref(describe(b)), _ref(describe(sfa)),
-                                            _ref(describe(sfb)), _ref(describe(d)), _ref(describe(masked_m)),
+    _check(lib.m_grouped_fp8_gemm_nt_masked(_arg(a), _arg(b), _arg(sfa),
+                                            _arg(sfb), _arg(d), _arg(masked_m),
                                             int(max_m_per_group), _stream(stream)))
     return d
 
@@ -284,19 +287,19 @@ def m_grouped_bf16_gemm_nt_masked(a, b, d, masked_m, max_m_per_group, stream=Non
     accumulate form d = c + a . b^T (m_grouped_bf16_gemm_nt_masked_acc)."""
     lib = load_library()
     if c is not None:
-        _check(lib.m_grouped_bf16_gemm_nt_masked_acc(_ref(describe(a)), _ref(describe(b)), _ref(describe(c)),
-                                                     _ref(describe(d)), _ref(describe(masked_m)), int(max_m_per_group),
+        _check(lib.m_grouped_bf16_gemm_nt_masked_acc(_arg(a), _arg(b), _arg(c),
+                                                     _arg(d), _arg(masked_m), int(max_m_per_group),
                                                      _stream(stream)))
         return d
-    _check(lib.m_grouped_bf16_gemm_nt_masked(_ref(describe(a)), _ref(describe(b)), _ref(describe(d)),
-                                             _ref(describe(masked_m)), int(max_m_per_group), _stream(stream)))
+    _check(lib.m_grouped_bf16_gemm_nt_masked(_arg(a), _arg(b), _arg(d),
+                                             _arg(masked_m), int(max_m_per_group), _stream(stream)))
     return d
 
 
 def bf16_gemm_nt(a, b, c, d, stream=None):
     """d = c + a . b^T in BF16 (FP32 accumulation); c is None or a BF16/F32 [M, N] tensor (may be d)."""
     lib = load_library()
-    _check(lib.bf16_gemm_nt(_ref(describe(a)), _ref(describe(b)), _ref(describe(c)), _ref(describe(d)),
+    _check(lib.bf16_gemm_nt(_arg(a), _arg(b), _arg(c), _arg(d),
                             _stream(stream)))
     return d
 
@@ -306,25 +309,25 @@ def m_grouped_bf16_gemm_nt_contiguous(a, b, d, grouped_layout, stream=None, c=No
     the accumulate form d = c + a . b^T (m_grouped_bf16_gemm_nt_contiguous_acc)."""
     lib = load_library()
     if c is not None:
-        _check(lib.m_grouped_bf16_gemm_nt_contiguous_acc(_ref(describe(a)), _ref(describe(b)), _ref(describe(c)),
-                                                         _ref(describe(d)), _ref(describe(grouped_layout)),
+        _check(lib.m_grouped_bf16_gemm_nt_contiguous_acc(_arg(a), _arg(b), _arg(c),
+                                                         _arg(d), _arg(grouped_layout),
                                                          _stream(stream)))
         return d
-    _check(lib.m_grouped_bf16_gemm_nt_contiguous(_ref(describe(a)), _ref(describe(b)), _ref(describe(d)),
-                                                 _ref(describe(grouped_layout)), _stream(stream)))
+    _check(lib.m_grouped_bf16_gemm_nt_contiguous(_arg(a), _arg(b), _arg(d),
+                                                 _arg(grouped_layout), _stream(stream)))
     return d
 
 
 def per_token_cast_to_fp8(x, q, sf, use_ue8m0=False, stream=None):
     lib = load_library()
-    _check(lib.per_token_cast_to_fp8(_ref(describe(x)), _ref(describe(q)), _ref(describe(sf)),
+    _check(lib.per_token_cast_to_fp8(_arg(x), _arg(q), _arg(sf),
                                      int(bool(use_ue8m0)), _stream(stream)))
     return q, sf
 
 
 def per_block_cast_to_fp8(x, q, sf, use_ue8m0=False, stream=None):
     lib = load_library()
-    _check(lib.per_block_cast_to_fp8(_ref(describe(x)), _ref(describe(q)), _ref(describe(sf)),
+    _check(lib.per_block_cast_to_fp8(_arg(x), _arg(q), _arg(sf),
                                      int(bool(use_ue8m0)), _stream(stream)))
     return q, sf
 
@@ -335,7 +338,7 @@ def pack_ue8m0_to_int(x, out, invalid_count=None, stream=None):
     number of non-UE8M0 inputs, added on the device."""
     lib = load_library()
     cnt = ctypes.c_void_p(invalid_count.data_ptr()) if invalid_count is not None else None
-    _check(lib.pack_ue8m0_to_int(_ref(describe(x)), _ref(describe(out)), cnt, _stream(stream)))
+    _check(lib.pack_ue8m0_to_int(_arg(x), _arg(out), cnt, _stream(stream)))
     return out
 
 
@@ -343,9 +346,9 @@ def moe_dispatch_masked_fp8(x, topk_idx, a, sfa, masked_m, slot, src, use_ue8m0=
     """Route (token, choice) pairs into the expert buffers a / sfa (masked
     layout) with the per-token FP8 cast; fills masked_m, slot and src."""
     lib = load_library()
-    _check(lib.moe_dispatch_masked_fp8(_ref(describe(x)), _ref(describe(topk_idx)), _ref(describe(a)),
-                                       _ref(describe(sfa)), _ref(describe(masked_m)), _ref(describe(slot)),
-                                       _ref(describe(src)), int(bool(use_ue8m0)), _stream(stream)))
+    _check(lib.moe_dispatch_masked_fp8(_arg(x), _arg(topk_idx), _arg(a),
+                                       _arg(sfa), _arg(masked_m), _arg(slot),
+                                       _arg(src), int(bool(use_ue8m0)), _stream(stream)))
     return a, sfa, masked_m, slot, src
 
 
@@ -355,16 +358,16 @@ def moe_dispatch_contiguous_fp8(x, topk_idx, a, sfa, grouped_layout, counts, slo
     whole `align`-row granules per expert, align 128 or 256) with the
     per-token FP8 cast; fills grouped_layout, counts and slot."""
     lib = load_library()
-    _check(lib.moe_dispatch_contiguous_fp8(_ref(describe(x)), _ref(describe(topk_idx)), _ref(describe(a)),
-                                           _ref(describe(sfa)), _ref(describe(grouped_layout)), _ref(describe(counts)),
-                                           _ref(describe(slot)), int(align), int(bool(use_ue8m0)), _stream(stream)))
+    _check(lib.moe_dispatch_contiguous_fp8(_arg(x), _arg(topk_idx), _arg(a),
+                                           _arg(sfa), _arg(grouped_layout), _arg(counts),
+                                           _arg(slot), int(align), int(bool(use_ue8m0)), _stream(stream)))
     return a, sfa, grouped_layout, counts, slot
 
 
 def moe_combine(d, slot, topk_weights, y, stream=None):
     """y[t] = sum_j topk_weights[t, j] * d[slot[t, j]] (BF16 out)."""
     lib = load_library()
-    _check(lib.moe_combine(_ref(describe(d)), _ref(describe(slot)), _ref(describe(topk_weights)), _ref(describe(y)),
+    _check(lib.moe_combine(_arg(d), _arg(slot), _arg(topk_weights), _arg(y),
                            _stream(stream)))
     return y
 
@@ -385,8 +388,8 @@ def moe_route_topk(logits, topk_idx, topk_weights, bias=None, score="softmax", n
     "sigmoid"; bias counts for the choice only; groups: the topk_group best of
     n_group ranges of experts by the sum of their group_top best choices."""
     lib = load_library()
-    _check(lib.moe_route_topk(_ref(describe(logits)), _ref(describe(bias)), _ref(describe(topk_idx)),
-                              _ref(describe(topk_weights)), _score_code(score), int(n_group), int(topk_group),
+    _check(lib.moe_route_topk(_arg(logits), _arg(bias), _arg(topk_idx),
+                              _arg(topk_weights), _score_code(score), int(n_group), int(topk_group),
                               int(group_top), int(bool(renormalize)), float(scale), _stream(stream)))
     return topk_idx, topk_weights
 
@@ -395,8 +398,8 @@ def moe_route_topk_bwd(logits, topk_idx, grad_weights, grad_logits, score="softm
                        stream=None):
     """grad_logits from the gradient of moe_route_topk's weights (the choice taken as given)."""
     lib = load_library()
-    _check(lib.moe_route_topk_bwd(_ref(describe(logits)), _ref(describe(topk_idx)), _ref(describe(grad_weights)),
-                                  _ref(describe(grad_logits)), _score_code(score), int(bool(renormalize)),
+    _check(lib.moe_route_topk_bwd(_arg(logits), _arg(topk_idx), _arg(grad_weights),
+                                  _arg(grad_logits), _score_code(score), int(bool(renormalize)),
                                   float(scale), _stream(stream)))
     return grad_logits
 
@@ -407,10 +410,10 @@ def kv_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_toke
     [pages, Hkv, P, D] (scales [pages, Hkv]), keys rotated by position with
     cos_sin [positions, rot]; q [T, Hq, D] is rotated into q_out on the way."""
     lib = load_library()
-    _check(lib.kv_append_fp8(_ref(describe(k)), _ref(describe(v)), _ref(describe(k_cache)), _ref(describe(v_cache)),
-                             _ref(describe(k_scale)), _ref(describe(v_scale)), _ref(describe(block_table)),
-                             _ref(describe(cu_tokens)), _ref(describe(start)), _ref(describe(cos_sin)),
-                             _ref(describe(q)), _ref(describe(q_out)), int(bool(interleaved)), _stream(stream)))
+    _check(lib.kv_append_fp8(_arg(k), _arg(v), _arg(k_cache), _arg(v_cache),
+                             _arg(k_scale), _arg(v_scale), _arg(block_table),
+                             _arg(cu_tokens), _arg(start), _arg(cos_sin),
+                             _arg(q), _arg(q_out), int(bool(interleaved)), _stream(stream)))
     return k_cache, v_cache, k_scale, v_scale
 
 
@@ -425,10 +428,10 @@ def paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_
     """Attention of the n newest tokens of each sequence, q [S, n, Hq, D],
     over its pages of the FP8 caches; lse [S, n, Hq] is optional."""
     lib = load_library()
-    _check(lib.paged_attention_fp8(_ref(describe(q)), _ref(describe(k_cache)), _ref(describe(v_cache)),
-                                   _ref(describe(k_scale)), _ref(describe(v_scale)), _ref(describe(block_table)),
-                                   _ref(describe(seq_lens)), _ref(describe(out)), _ref(describe(lse)),
-                                   _ref(describe(workspace)), float(scale), int(window), _stream(stream)))
+    _check(lib.paged_attention_fp8(_arg(q), _arg(k_cache), _arg(v_cache),
+                                   _arg(k_scale), _arg(v_scale), _arg(block_table),
+                                   _arg(seq_lens), _arg(out), _arg(lse),
+                                   _arg(workspace), float(scale), int(window), _stream(stream)))
     return out
 
 

@@ -1288,9 +1288,7 @@ int kv_append_fp8(const dg_tensor* k, const dg_tensor* v, const dg_tensor* k_cac
   p.Hq = (int32_t)Hq;
   p.D = (int32_t)D;
   p.P = (int32_t)P;
-  int64_t kv_blocks;
-  int by_token;
-  if (dgmi::kv_append_grid(T, S, P, Hkv, p.q != nullptr, &kv_blocks, &by_token) > kMaxGroups)
+  if (dgmi::kv_append_plan(T, S, P, Hkv, D, p.q != nullptr).grid > kMaxGroups)
     return fail(DG_UNSUPPORTED, "%s: too many tokens times heads for one launch", fname);
   return check_launch(dgmi::launch_kv_append(p, stream), fname);
 }

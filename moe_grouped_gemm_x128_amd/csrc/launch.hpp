@@ -132,8 +132,16 @@ struct KvAppendArgs {
   int32_t max_pages, pages;
   const int32_t *cu, *start;
   int32_t T, S, Hkv, Hq, D, P;
-  int64_t kv_blocks;  // set by the launcher
-  int32_t by_token;   // set by the launcher
+  // set by the launcher: workgroups before those of q, workgroups of a page
+  // slot, kinds (a head's K or V) of a workgroup, tokens of q of a workgroup,
+  // one slot per token (else per page), log2 P
+  int64_t kv_blocks;
+  int32_t kind_blocks, kinds, q_tokens, by_token, log_p;
+};
+
+struct KvAppendPlan {
+  int64_t grid, kv_blocks, kind_blocks, kinds, q_tokens;
+  bool by_token;
 };
 
 // Attention over the paged FP8 cache (attn.hip): q and out [S, n, Hq, D],
@@ -184,7 +192,7 @@ hipError_t launch_moe_route_contiguous(const MoeRouteArgs& p, hipStream_t stream
 hipError_t launch_moe_combine(const MoeCombineArgs& p, hipStream_t stream);
 hipError_t launch_moe_route_topk(RouteTopkArgs p, hipStream_t stream);
 hipError_t launch_moe_route_topk_bwd(RouteTopkBwdArgs p, hipStream_t stream);
-int64_t kv_append_grid(int64_t T, int64_t S, int64_t P, int64_t Hkv, bool q, int64_t* kv_blocks, int* by_token);
+KvAppendPlan kv_append_plan(int64_t T, int64_t S, int64_t P, int64_t Hkv, int64_t D, bool q);
 hipError_t launch_kv_append(KvAppendArgs p, hipStream_t stream);
 int64_t paged_attention_workspace(int64_t S, int64_t n, int64_t Hq, int64_t Hkv, int64_t D, int64_t cap);
 // largest grid of the call's kernels
