@@ -433,11 +433,13 @@ int moe_route_topk_bwd(const dg_tensor* logits, const dg_tensor* topk_idx, const
  *   k, v         F32 or BF16 [T, Hkv, D], the sequences' new tokens one after
  *                another; D = 64, 128 or 256
  *   k_cache, v_cache  E4M3 [pages, Hkv, P, D], P = 16, 32, 64 or 128; any
- *                strides that are multiples of 16 (innermost 1): pages may be
+ *                strides that are multiples of 16 (innermost 1; tokens less
+ *                than 2^24 bytes apart, pages less than 2^32): pages may be
  *                laid out head by head or token by token, and the two caches
  *                may be halves of one pool
- *   k_scale, v_scale  F32 [pages, Hkv], any strides: the scale of each page
- *                and head, a power of two
+ *   k_scale, v_scale  F32 [pages, Hkv], any strides (pages less than 2^30
+ *                elements apart): the scale of each page and head, a power of
+ *                two
  *   block_table  I32 [S, max_pages]: the pages of each sequence, in order
  *   cu_tokens    I32 [S + 1]: sequence s brings tokens cu[s] .. cu[s+1]-1
  *   start        I32 [S]: how many tokens of it are in the cache already, so

@@ -1030,8 +1030,11 @@ int check_cache(const dg_tensor* c, const char* name, const dg_tensor* sc, const
     return fail(DG_UNSUPPORTED, "%s: page size %lld is not 16, 32, 64 or 128", fname, (long long)P);
   if (!aligned(c->data, 16) || c->stride[0] % 16 || c->stride[1] % 16 || c->stride[2] % 16)
     return fail(DG_INVALID_ARG, "%s: %s needs a 16-byte aligned base and strides", fname, name);
-  if (c->stride[2] >= (int64_t(1) << 26))  // 32-bit offsets inside 16 tokens
-    return fail(DG_UNSUPPORTED, "%s: the token stride of %s must be below 2^26 bytes", fname, name);
+  // (a page's tokens and the page strides are reached with 32-bit offsets)
+  if (c->stride[2] >= (int64_t(1) << 24) || (c->shape[0] > 1 && c->stride[0] >= (int64_t(1) << 32)) ||
+      (sc->shape[0] > 1 && sc->stride[0] >= (int64_t(1) << 30)))
+    return fail(DG_UNSUPPORTED, "%s: the token stride of %s must be below 2^24 bytes, its page stride below 2^32 bytes "
+                "and that of %s below 2^30 elements", fname, name, sname);
   return DG_OK;
 }
 
@@ -1334,8 +1337,9 @@ int paged_attention_fp8(const dg_tensor* q, const dg_tensor* k_cache, const dg_t
   if (rows > INT32_MAX - 16 || Hkv * row_tiles > INT32_MAX ||
       (row_tiles > 0 && dgmi::paged_attention_grid(S, Hkv, row_tiles, D, block_table->shape[1] * P) > kMaxGroups))
     return fail(DG_UNSUPPORTED, "%s: too many queries for one launch", fname);
-  if (Hkv * row_tiles * (block_table->shape[1] * P / 32 + 1) > INT32_MAX)
-    return fail(DG_UNSUPPORTED, "%s: too many tokens times heads for one sequence", fname);
+  // the work is counted in 32-token tiles of every head and 16 query rows, in 31 bits
+  if (S * Hkv * row_tiles > INT32_MAX || S * Hkv * row_tiles * (block_table->shape[1] * P / 32 + 1) > INT32_MAX - 65536)
+    return fail(DG_UNSUPPORTED, "%s: too many tokens times heads for one call", fname);
   const int64_t need = paged_attention_fp8_workspace(S, n, Hq, Hkv, D, block_table->shape[1] * P);
   if (need > 0) {
     if (workspace == nullptr) return fail(DG_INVALID_ARG, "%s: workspace of %lld bytes needed", fname, (long long)need);
@@ -1372,17 +1376,17 @@ int paged_attention_fp8(const dg_tensor* q, const dg_tensor* k_cache, const dg_t
   }
   p.k_cache = static_cast<const uint8_t*>(k_cache->data);
   p.v_cache = static_cast<const uint8_t*>(v_cache->data);
-  p.skc_p = k_cache->stride[0];
+  p.skc_p = (uint32_t)k_cache->stride[0];
   p.skc_h = k_cache->stride[1];
-  p.skc_t = k_cache->stride[2];
-  p.svc_p = v_cache->stride[0];
+  p.skc_t = (uint32_t)k_cache->stride[2];
+  p.svc_p = (uint32_t)v_cache->stride[0];
   p.svc_h = v_cache->stride[1];
-  p.svc_t = v_cache->stride[2];
+  p.svc_t = (uint32_t)v_cache->stride[2];
   p.k_scale = static_cast<const float*>(k_scale->data);
   p.v_scale = static_cast<const float*>(v_scale->data);
-  p.sks_p = k_scale->stride[0];
+  p.sks_p = (uint32_t)(k_scale->stride[0] * 4);
   p.sks_h = k_scale->stride[1];
-  p.svs_p = v_scale->stride[0];
+  p.svs_p = (uint32_t)(v_scale->stride[0] * 4);
   p.svs_h = v_scale->stride[1];
   p.table = static_cast<const int32_t*>(block_table->data);
   p.s_table = block_table->stride[0];

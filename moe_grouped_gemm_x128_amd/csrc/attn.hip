@@ -51,6 +51,9 @@ typedef float f32x2 __attribute__((ext_vector_type(2)));
 
 constexpr int ATTN_WAVES = 4;
 constexpr int ATTN_THREADS = 64 * ATTN_WAVES;
+// Waves per SIMD that the registers are held to: the output takes D / 4 MT
+// registers of a lane, the queries D / 8 MT, a tile's codes D / 4.
+constexpr int WAVES_PER_SIMD(int D, int MT) { return D * MT <= 128 ? 3 : 2; }
 constexpr float P_SHIFT = 14.0f;  // weights are held times 2^14
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
 
@@ -86,77 +89,83 @@ __device__ __forceinline__ Span span_of(const PagedAttnArgs& p, int len) {
   return Span{len, begin, end > begin ? end : begin + 1};
 }
 
-// Tiles of sequence s on the line of all units' tiles.
-__device__ __forceinline__ int64_t line_tiles(const PagedAttnArgs& p, int s) {
-  if (s >= p.S) return 0;
-  const Span sp = span_of(p, p.lens[s]);
-  return (int64_t)(sp.end - sp.begin) * p.units;
+// Inclusive prefix sum over the wave's lanes: within rows of 16 by DPP shifts,
+// then the rows' last lanes passed on.
+__device__ __forceinline__ int wave_scan(int v) {
+  v += __builtin_amdgcn_update_dpp(0, v, 0x111, 0xf, 0xf, false);  // row shift right by 1, 2, 4, 8
+  v += __builtin_amdgcn_update_dpp(0, v, 0x112, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x114, 0xf, 0xf, false);
+  v += __builtin_amdgcn_update_dpp(0, v, 0x118, 0xf, 0xf, false);
+  const int r0 = __builtin_amdgcn_readlane(v, 15), r1 = __builtin_amdgcn_readlane(v, 31), r2 = __builtin_amdgcn_readlane(v, 47);
+  const int row = (threadIdx.x >> 4) & 3;
+  return v + (row > 0 ? r0 : 0) + (row > 1 ? r1 : 0) + (row > 2 ? r2 : 0);
 }
 
 // Inclusive prefix sum of v over the workgroup; *all gets the total.
-__device__ __forceinline__ int64_t line_scan(int64_t v, int64_t* red, int64_t* all) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-#pragma unroll
-  for (int off = 1; off < 64; off <<= 1) {
-    const int64_t up = __shfl_up(v, off, 64);
-    if (lane >= off) v += up;
-  }
+__device__ __forceinline__ int line_scan(int v, int* red, int* all) {
+  const int wave = threadIdx.x >> 6;
+  v = wave_scan(v);
   __syncthreads();  // the last scan's sums have been read
-  if (lane == 63) red[wave] = v;
+  if ((threadIdx.x & 63) == 63) red[wave] = v;
   __syncthreads();
-  int64_t total = 0;
+  int total = 0;
 #pragma unroll
   for (int w = 0; w < ATTN_WAVES; ++w) {
     v += w < wave ? red[w] : 0;
     total += red[w];
   }
-  *all = total;
+  *all = uniform(total);
   return v;
 }
 
-__device__ __forceinline__ int64_t uniform64(int64_t v) {
-  return (int64_t)((uint64_t)(uint32_t)uniform((int)(v & 0xffffffff)) | ((uint64_t)(uint32_t)uniform((int)(v >> 32)) << 32));
+// Tiles of sequence s on the line of all units' tiles (the line is below 2^31).
+__device__ __forceinline__ int line_tiles(const PagedAttnArgs& p, int s, int* len) {
+  *len = s < p.S ? p.lens[s] : 0;
+  const Span sp = span_of(p, *len);
+  return s < p.S ? (sp.end - sp.begin) * p.units : 0;
 }
 
-// This workgroup's share [*at, *end) of the line (false: nothing), the
-// sequence in which it begins and the tiles before that one.
-__device__ __forceinline__ bool line_share(const PagedAttnArgs& p, int64_t* red, int64_t* found, int64_t* share,
-                                           int64_t* at, int64_t* end, int* s_out, int64_t* before_out) {
-  int64_t mine = line_tiles(p, threadIdx.x), total;
-  int64_t upto = line_scan(mine, red, &total);
+// This workgroup's part [at, end) of the line, the sequence in which it begins
+// and the tiles before that one.
+struct Share {
+  int size, at, end, before, s, len;
+};
+
+// false: nothing for this workgroup.
+__device__ __forceinline__ bool line_share(const PagedAttnArgs& p, int* red, int* found, Share& o) {
+  int len, total;
+  int mine = line_tiles(p, threadIdx.x, &len);
+  int upto = line_scan(mine, red, &total);
   for (int base = ATTN_THREADS; base < p.S; base += ATTN_THREADS) {  // (more sequences than threads)
-    int64_t all;
-    line_scan(line_tiles(p, base + threadIdx.x), red, &all);
+    int l, all;
+    line_scan(line_tiles(p, base + threadIdx.x, &l), red, &all);
     total += all;
   }
-  total = uniform64(total);
-  int64_t n = (total + p.shares - 1) / p.shares;
-  if (n < p.min_share) n = p.min_share;
-  *share = n;
-  *at = blockIdx.x * n;
-  *end = *at + n < total ? *at + n : total;
-  if (*at >= *end) return false;
-  int64_t before = 0;
+  const int n = (int)(((uint32_t)total + p.shares - 1) / p.shares);
+  o.size = n < p.min_share ? p.min_share : n;
+  const int64_t at = (int64_t)blockIdx.x * o.size;
+  if (at >= total) return false;
+  o.at = (int)at;
+  o.end = at + o.size < total ? o.at + o.size : total;
+  int before = 0;
   for (int base = 0;; base += ATTN_THREADS) {
-    if (base > 0) {
-      int64_t all;
-      mine = line_tiles(p, base + threadIdx.x);
+    if (p.S > ATTN_THREADS) {
+      int all;
+      mine = line_tiles(p, base + threadIdx.x, &len);
       upto = before + line_scan(mine, red, &all);
       before += all;
-    } else if (p.S > ATTN_THREADS) {
-      int64_t all;
-      upto = line_scan(mine, red, &all);
-      before = all;
     }
-    if (*at >= upto - mine && *at < upto) {
-      found[0] = base + (int)threadIdx.x;
+    if (o.at >= upto - mine && o.at < upto) {
+      found[0] = base + threadIdx.x;
       found[1] = upto - mine;
+      found[2] = len;
     }
-    if (p.S <= ATTN_THREADS || *at < before) break;
+    if (p.S <= ATTN_THREADS || o.at < before) break;
   }
   __syncthreads();
-  *s_out = uniform((int)found[0]);
-  *before_out = uniform64(found[1]);
+  o.s = uniform(found[0]);
+  o.before = uniform(found[1]);
+  o.len = uniform(found[2]);
   return true;
 }
 
@@ -168,27 +177,40 @@ struct Heads {
   int len;
 };
 
-// Where a tile's two 16-token halves lie, and their scales: one page each.
-struct TileRef {
-  int page[2];  // 0 where the half takes no part
+// The pages of a tile's two 16-token halves as the table has them, -1 past
+// the end.  One load where a page holds 32 tokens or more (the second is then
+// the first).
+struct Pages {
+  int id0, id1;
+};
+__device__ __forceinline__ void find_pages(const PagedAttnArgs& p, const Heads& hd, int t, bool wanted, Pages& x) {
+  x.id0 = x.id1 = -1;
+  if (wanted && t * 32 < hd.len) x.id0 = uniform_load(hd.table + ((t * 32) >> p.log_p));
+  if (p.P == 16 && wanted && t * 32 + 16 < hd.len) x.id1 = uniform_load(hd.table + 2 * t + 1);
+}
+
+// Where a tile's halves are, and their scales (1 where a half takes no part:
+// its page is outside the pool, and page 0 is read instead).
+struct Place {
+  int page[2];
   float ks[2], vs[2];
   bool ok[2];
 };
+// One page's place: strides are below 2^32 bytes, a page's tokens within 2^31.
+__device__ __forceinline__ uint64_t page_offset(int page, uint32_t stride) { return (uint64_t)(uint32_t)page * stride; }
 
-__device__ __forceinline__ void find_tile(const PagedAttnArgs& p, const Heads& hd, int t, bool wanted, TileRef& x) {
+__device__ __forceinline__ float page_scale(const float* base, int page, uint32_t stride, bool ok) {
+  const int v = uniform_load(reinterpret_cast<const int32_t*>(reinterpret_cast<const uint8_t*>(base) + page_offset(page, stride)));
+  return __int_as_float(ok ? v : 0x3f800000);
+}
+__device__ __forceinline__ void place_tile(const PagedAttnArgs& p, const Heads& hd, const Pages& pages, Place& x) {
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const int at = t * 32 + 16 * u;
-    int page = -1;
-    if (wanted && at < hd.len) page = uniform_load(hd.table + (at >> p.log_p));
-    x.ok[u] = page >= 0 && page < p.pages;
-    x.ks[u] = x.vs[u] = 1.0f;
-    x.page[u] = 0;
-    if (x.ok[u]) {
-      x.page[u] = page;
-      x.ks[u] = uniform_load(hd.ks + page * p.sks_p);
-      x.vs[u] = uniform_load(hd.vs + page * p.svs_p);
-    }
+    const int id = u == 0 || p.P > 16 ? pages.id0 : pages.id1;
+    x.ok[u] = id >= 0 && id < p.pages;
+    x.page[u] = x.ok[u] ? id : 0;
+    x.ks[u] = page_scale(hd.ks, x.page[u], p.sks_p, x.ok[u]);
+    x.vs[u] = page_scale(hd.vs, x.page[u], p.svs_p, x.ok[u]);
   }
 }
 
@@ -199,17 +221,42 @@ struct Tile {
   int v[2][4][D / 64];  // D / 16 bytes of four tokens in each half
 };
 
+// lane: this lane's offset inside a 16-token half.  (Kept opaque, so that the
+// loads take a scalar base and a 32-bit offset.)
 template <int D>
-__device__ __forceinline__ void load_v(const PagedAttnArgs& p, const Heads& hd, int t, const TileRef& ref,
-                                       uint32_t v_lane, Tile<D>& x) {
-  constexpr int VB = D / 16;
+__device__ __forceinline__ void load_k(const PagedAttnArgs& p, const Heads& hd, int t, const Place& at, uint32_t lane,
+                                       Tile<D>& x) {
+  asm volatile("" : "+v"(lane));
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int slot = (t * 32 + 16 * u) & (p.P - 1);
-    const uint8_t* vp = hd.v + ref.page[u] * p.svc_p + slot * p.svc_t;
+    const uint8_t* kp = hd.k + page_offset(at.page[u], p.skc_p) + slot * p.skc_t;
+#pragma unroll
+    for (int j = 0; j < D / 64; ++j) {
+      const i32x4 v = *reinterpret_cast<const i32x4*>(kp + lane + 16 * j);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x.k[u][4 * j + e] = v[e];
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void load_v(const PagedAttnArgs& p, const Heads& hd, int t, const Place& at, uint32_t lane,
+                                       Tile<D>& x) {
+  constexpr int VB = D / 16;
+  uint32_t off[4];
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    off[e] = lane + e * p.svc_t;
+    asm volatile("" : "+v"(off[e]));
+  }
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int slot = (t * 32 + 16 * u) & (p.P - 1);
+    const uint8_t* vp = hd.v + page_offset(at.page[u], p.svc_p) + slot * p.svc_t;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      const uint8_t* row = vp + e * p.svc_t + v_lane;
+      const uint8_t* row = vp + off[e];
       if constexpr (VB == 4) {
         x.v[u][e][0] = *reinterpret_cast<const int*>(row);
       } else if constexpr (VB == 8) {
@@ -225,24 +272,6 @@ __device__ __forceinline__ void load_v(const PagedAttnArgs& p, const Heads& hd, 
   }
 }
 
-template <int D>
-__device__ __forceinline__ void load_tile(const PagedAttnArgs& p, const Heads& hd, int t, const TileRef& ref,
-                                          uint32_t k_lane, uint32_t v_lane, Tile<D>& x) {
-  constexpr int KB = D / 4;
-#pragma unroll
-  for (int u = 0; u < 2; ++u) {
-    const int slot = (t * 32 + 16 * u) & (p.P - 1);
-    const uint8_t* kp = hd.k + ref.page[u] * p.skc_p + slot * p.skc_t;
-#pragma unroll
-    for (int j = 0; j < KB / 16; ++j) {
-      const i32x4 v = *reinterpret_cast<const i32x4*>(kp + k_lane + 16 * j);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) x.k[u][4 * j + e] = v[e];
-    }
-  }
-  load_v<D>(p, hd, t, ref, v_lane, x);
-}
-
 // Running state of one wave: rows = lane & 15, each lane a quarter of a row's
 // output (elements (lane / 16) * D/4 ...), and its own part of the row's sum.
 template <int D>
@@ -251,71 +280,84 @@ struct RowState {
   float m, l;
 };
 
-// What the 16 rows of a unit look at.
+// The positions that this lane's row of a row tile sees, [see_lo, see_hi].
 struct Rows {
-  int qi, see_lo, see_hi;            // this lane's row
-  int qi_first, qi_last;             // query positions of the tile
-  int lo_all, hi_all;                // positions that every row sees
+  int see_lo, see_hi;
 };
 
-// Scores and weights of a tile: the running maximum and sum move on, the
-// output so far is scaled to the new maximum; returns P^T as the second
-// product wants it.  whole: every row sees all 32 positions.
-template <int D>
-__device__ __forceinline__ f16x8 weigh(const Tile<D>& x, const TileRef& ref, const bf16x8 (&q)[D / 32], const Rows& r,
-                                       bool whole, int t, int g4, float qk, RowState<D>& st) {
-  // S^T: lane = its row, tokens 16 u + 4 g4 + i
-  f32x4 sc[2];
+// A row's value from its four lanes (l, l + 16, l + 32, l + 48): a swap of two
+// copies leaves both values of a pair in every lane.
+template <typename F>
+__device__ __forceinline__ float quarters(float v, F f) {
+  const auto r = __builtin_amdgcn_permlane16_swap(__float_as_int(v), __float_as_int(v), false, false);
+  v = f(__int_as_float(r[0]), __int_as_float(r[1]));
+  const auto h = __builtin_amdgcn_permlane32_swap(__float_as_int(v), __float_as_int(v), false, false);
+  return f(__int_as_float(h[0]), __int_as_float(h[1]));
+}
+
+// S^T of a tile: lane = its row, tokens 16 u + 4 g4 + i.
+template <int D, int MT>
+__device__ __forceinline__ void scores(const Tile<D>& x, const bf16x8 (&q)[MT][D / 32], f32x4 (&sc)[MT][2]) {
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+    for (int k = 0; k < MT; ++k) sc[k][u] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
     for (int j = 0; j < D / 32; ++j) {
       const i32x2 a = fp8x4_to_bf16(x.k[u][2 * j]), b = fp8x4_to_bf16(x.k[u][2 * j + 1]);
       const bf16x8 kf = __builtin_bit_cast(bf16x8, i32x4{a[0], a[1], b[0], b[1]});
-      acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[j], acc, 0, 0, 0);
+#pragma unroll
+      for (int k = 0; k < MT; ++k) sc[k][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(kf, q[k][j], sc[k][u], 0, 0, 0);
     }
-    sc[u] = acc;
   }
-  float y[8], inv[2];
+}
+
+// Weights of a tile: the running maxima and sums move on, the outputs so far
+// are scaled to the new maxima; pf gets P^T as the second product wants it.
+// whole: every row sees all 32 positions.
+template <int D, int MT>
+__device__ __forceinline__ void weigh(const f32x4 (&sc)[MT][2], const Place& x, const Rows (&r)[MT], bool whole, int t,
+                                      int g4, float qk, RowState<D> (&st)[MT], f16x8 (&pf)[MT]) {
+  float lsv[2], inv[2];
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const float lsv = __builtin_amdgcn_logf(ref.vs[u]);
-    inv[u] = __builtin_amdgcn_rcpf(ref.vs[u]);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[4 * u + i] = __builtin_fmaf(sc[u][i], ref.ks[u] * qk, lsv);
+    lsv[u] = __builtin_amdgcn_logf(x.vs[u]);
+    inv[u] = __builtin_amdgcn_rcpf(x.vs[u]);
   }
-  if (!whole) {
+#pragma unroll
+  for (int k = 0; k < MT; ++k) {
+    float y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = __builtin_fmaf(sc[k][i / 4][i % 4], x.ks[i / 4] * qk, lsv[i / 4]);
+    if (!whole) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const int at = t * 32 + 16 * (i / 4) + 4 * g4 + i % 4;
+        y[i] = x.ok[i / 4] && at >= r[k].see_lo && at <= r[k].see_hi ? y[i] : -INFINITY;
+      }
+    }
+    float mx = y[0];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) mx = fmaxf(mx, y[i]);
+    mx = quarters(mx, [](float a, float b) { return fmaxf(a, b); });
+    const float m_new = fmaxf(st[k].m, mx);
+    const float m_use = m_new == -INFINITY ? 0.0f : m_new - P_SHIFT;  // nothing seen so far
+    if (__any(m_new != st[k].m)) {  // (seldom, once the largest scores have been seen)
+      const float alpha = __builtin_amdgcn_exp2f(st[k].m - P_SHIFT - m_use);
+      st[k].m = m_new;
+      st[k].l *= alpha;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) st[k].o[i][e] *= alpha;
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int at = t * 32 + 16 * (i / 4) + 4 * g4 + i % 4;
-      y[i] = ref.ok[i / 4] && at >= r.see_lo && at <= r.see_hi ? y[i] : -INFINITY;
+      const float w = __builtin_amdgcn_exp2f(y[i] - m_use);
+      st[k].l = __builtin_fmaf(w, inv[i / 4], st[k].l);
+      pf[k][i] = (_Float16)w;
     }
   }
-  float mx = y[0];
-#pragma unroll
-  for (int i = 1; i < 8; ++i) mx = fmaxf(mx, y[i]);
-  mx = fmaxf(mx, __shfl_xor(mx, 16, 64));
-  mx = fmaxf(mx, __shfl_xor(mx, 32, 64));
-  const float m_new = fmaxf(st.m, mx);
-  const float m_use = m_new == -INFINITY ? 0.0f : m_new - P_SHIFT;  // nothing seen so far
-  if (__any(m_new != st.m)) {  // (seldom, once the largest scores have been seen)
-    const float alpha = __builtin_amdgcn_exp2f(st.m - P_SHIFT - m_use);
-    st.m = m_new;
-    st.l *= alpha;
-#pragma unroll
-    for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) st.o[i][e] *= alpha;
-  }
-  f16x8 pf;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float w = __builtin_amdgcn_exp2f(y[i] - m_use);
-    st.l = __builtin_fmaf(w, inv[i / 4], st.l);
-    pf[i] = (_Float16)w;
-  }
-  return pf;
 }
 
 // Elements 2b and 2b + 1 of a lane's eight tokens, in FP16.
@@ -335,25 +377,28 @@ __device__ __forceinline__ void turn_values(const Tile<D>& x, int b, f16x8& v0, 
 }
 
 // O^T += V^T P^T.
-template <int D>
-__device__ __forceinline__ void add_values(const Tile<D>& x, f16x8 pf, RowState<D>& st) {
+template <int D, int MT>
+__device__ __forceinline__ void add_values(const Tile<D>& x, const f16x8 (&pf)[MT], RowState<D> (&st)[MT]) {
 #pragma unroll
   for (int b = 0; b < D / 32; ++b) {
     f16x8 v0, v1;
     turn_values<D>(x, b, v0, v1);
-    st.o[2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf, st.o[2 * b], 0, 0, 0);
-    st.o[2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf, st.o[2 * b + 1], 0, 0, 0);
+#pragma unroll
+    for (int k = 0; k < MT; ++k) {
+      st[k].o[2 * b] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, pf[k], st[k].o[2 * b], 0, 0, 0);
+      st[k].o[2 * b + 1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, pf[k], st[k].o[2 * b + 1], 0, 0, 0);
+    }
   }
 }
 
 // Clears the values of positions outside [lo, hi] and of absent pages: their
 // codes may be NaN, and a weight of 0 would not hide that.
 template <int D>
-__device__ __forceinline__ void clear_values(const TileRef& ref, int t, int g4, int lo, int hi, Tile<D>& x) {
+__device__ __forceinline__ void clear_values(const Place& place, int t, int g4, int lo, int hi, Tile<D>& x) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int at = t * 32 + 16 * (i / 4) + 4 * g4 + i % 4;
-    const bool seen = ref.ok[i / 4] && at >= lo && at <= hi;
+    const bool seen = place.ok[i / 4] && at >= lo && at <= hi;
 #pragma unroll
     for (int b = 0; b < D / 64; ++b) x.v[i / 4][i % 4][b] = seen ? x.v[i / 4][i % 4][b] : 0;
   }
@@ -363,9 +408,9 @@ __device__ __forceinline__ void clear_values(const TileRef& ref, int t, int g4, 
 // values: it has to reach the rows that see it and no others, though a
 // weight of 0 times NaN is NaN.  The NaN codes are cleared, and a product of
 // their places with what each row sees says which outputs they make NaN.
-template <int D>
-__device__ __forceinline__ void take_out_nans(const TileRef& ref, const Rows& r, int t, int g4, Tile<D>& x,
-                                              RowState<D>& st) {
+template <int D, int MT>
+__device__ __forceinline__ void take_out_nans(const Place& place, const Rows (&r)[MT], int t, int g4, Tile<D>& x,
+                                              RowState<D> (&st)[MT]) {
   Tile<D> places;  // code 1 (a positive value) where there is a NaN
   int hit = 0;
 #pragma unroll
@@ -379,24 +424,30 @@ __device__ __forceinline__ void take_out_nans(const TileRef& ref, const Rows& r,
       w &= (int)~((uint32_t)n * 0xffu);
     }
   if (!__any(hit != 0)) return;
-  f16x8 sees;
+  f16x8 sees[MT];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const int at = t * 32 + 16 * (i / 4) + 4 * g4 + i % 4;
-    sees[i] = (_Float16)(ref.ok[i / 4] && at >= r.see_lo && at <= r.see_hi ? 1.0f : 0.0f);
-  }
+  for (int k = 0; k < MT; ++k)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int at = t * 32 + 16 * (i / 4) + 4 * g4 + i % 4;
+      sees[k][i] = (_Float16)(place.ok[i / 4] && at >= r[k].see_lo && at <= r[k].see_hi ? 1.0f : 0.0f);
+    }
 #pragma unroll
   for (int b = 0; b < D / 32; ++b) {
     f16x8 v0, v1;
     turn_values<D>(places, b, v0, v1);
-    const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
-    const f32x4 c0 = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, sees, zero, 0, 0, 0);
-    const f32x4 c1 = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, sees, zero, 0, 0, 0);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      st.o[2 * b][e] = c0[e] > 0.0f ? __uint_as_float(0x7fc00000u) : st.o[2 * b][e];
-      st.o[2 * b + 1][e] = c1[e] > 0.0f ? __uint_as_float(0x7fc00000u) : st.o[2 * b + 1][e];
+    for (int k = 0; k < MT; ++k) {
+      const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+      const f32x4 c0 = __builtin_amdgcn_mfma_f32_16x16x32_f16(v0, sees[k], zero, 0, 0, 0);
+      const f32x4 c1 = __builtin_amdgcn_mfma_f32_16x16x32_f16(v1, sees[k], zero, 0, 0, 0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        st[k].o[2 * b][e] = c0[e] > 0.0f ? __uint_as_float(0x7fc00000u) : st[k].o[2 * b][e];
+        st[k].o[2 * b + 1][e] = c1[e] > 0.0f ? __uint_as_float(0x7fc00000u) : st[k].o[2 * b + 1][e];
+      }
     }
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
@@ -422,155 +473,180 @@ __device__ __forceinline__ void store_row(const PagedAttnArgs& p, int s, int h, 
         l != 0.0f ? (m - P_SHIFT + __builtin_amdgcn_logf(l)) * LN2 : -INFINITY;
 }
 
-// A workgroup's waves: rt of them take the unit's row tiles side by side (the
-// second and later ones find the codes in the caches), ATTN_WAVES / rt streams
-// take the tiles of the line in turn.
-template <int D, bool SPLIT>
-__global__ __launch_bounds__(ATTN_THREADS, D > 128 ? 2 : 3) void paged_attention_kernel(const PagedAttnArgs p) {
+// MT: row tiles of a wave: the codes are converted once for up to 16 MT rows.
+// A unit with more rows has them spread over wr waves side by side (the second
+// and later ones find the codes in the caches); the ATTN_WAVES / wr streams of
+// waves take the tiles in turn.
+template <int D, int MT, bool SPLIT>
+__global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_attention_kernel(const PagedAttnArgs p) {
   constexpr int KB = D / 4;    // bytes of a key per lane
   constexpr int VB = D / 16;   // bytes of a value per lane, and output tiles
   constexpr int CW = D < 128 ? D : 128;  // columns that the waves join at a time
   __shared__ float so[ATTN_WAVES][16][CW + 4];
-  __shared__ float sm[ATTN_WAVES][16], sl[ATTN_WAVES][16];
-  __shared__ int64_t red[ATTN_WAVES], found[2];
+  __shared__ float sm[MT][ATTN_WAVES][16], sl[MT][ATTN_WAVES][16];
+  __shared__ int red[ATTN_WAVES], found[3];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int r16 = lane & 15, g4 = lane >> 4;
   const uint32_t k_lane = (uint32_t)(r16 * p.skc_t + g4 * KB);
   const uint32_t v_lane = (uint32_t)(4 * g4 * p.svc_t + r16 * VB);
   const float qk = p.scale * LOG2E;
-  const int streams = uniform(ATTN_WAVES / p.rt), stream = uniform(wave / p.rt);
+  const int streams = uniform(ATTN_WAVES / p.wr), stream = uniform(wave / p.wr), wgroup = wave - stream * p.wr;
 
-  int64_t share = 0, at = 0, end = 1, before = 0;
-  int s = uniform(blockIdx.x / p.units);
-  if (SPLIT && !line_share(p, red, found, &share, &at, &end, &s, &before)) return;
+  Share line = {0, 0, 1, 0, 0, 0};
+  if (SPLIT) {
+    if (!line_share(p, red, found, line)) return;
+  } else {
+    line.s = uniform(blockIdx.x / p.units);
+    line.len = uniform_load(p.lens + line.s);
+  }
 
-  while (at < end) {
-    const Span sp = span_of(p, uniform_load(p.lens + s));
+  while (line.at < line.end) {
+    const int s = line.s;
+    const Span sp = span_of(p, line.len);
     const int nt = sp.end - sp.begin;
-    if (SPLIT && at - before >= (int64_t)nt * p.units) {  // next sequence
-      before += (int64_t)nt * p.units;
-      ++s;
+    if (SPLIT && line.at - line.before >= nt * p.units) {  // next sequence
+      line.before += nt * p.units;
+      ++line.s;
+      line.len = uniform_load(p.lens + line.s);
       continue;
     }
-    const int rel = (int)(at - before);
+    const int rel = line.at - line.before;
     const int unit = uniform(SPLIT ? rel / nt : (int)(blockIdx.x - s * p.units));
     const int t0 = SPLIT ? rel - unit * nt : 0;
-    const int t1 = SPLIT && end - at < nt - t0 ? t0 + (int)(end - at) : nt;
-    const int h = uniform(unit / p.groups), row0 = (unit - h * p.groups) * p.rt * 16;
+    const int t1 = SPLIT && line.end - line.at < nt - t0 ? t0 + line.end - line.at : nt;
+    const int h = uniform(unit / p.groups), row0 = (unit - h * p.groups) * p.wr * MT * 16;
     const int len = sp.len;
 
-    // this lane's row: query position and the range of positions it sees
-    const int first_row = row0 + (wave - stream * p.rt) * 16;
-    const int row = first_row + r16;
-    const bool row_ok = row < p.rows;
-    const int qh = h * p.group + (row_ok ? row % p.group : 0);
-    const int last_row = first_row + 15 < p.rows ? first_row + 15 : p.rows - 1;
-    Rows r;
-    r.qi = row_ok ? row / p.group : 0;
-    r.qi_first = uniform(first_row / p.group);
-    r.qi_last = uniform(last_row / p.group);
-    const int qpos = len - p.n + r.qi;
-    r.see_hi = row_ok ? qpos : -1;
-    r.see_lo = p.window > 0 && qpos - p.window + 1 > 0 ? qpos - p.window + 1 : 0;
-    r.hi_all = len - p.n + r.qi_first;
-    const int hi_any = len - p.n + r.qi_last;
-    const int lo_any = p.window > 0 && r.hi_all - p.window + 1 > 0 ? r.hi_all - p.window + 1 : 0;
-    r.lo_all = p.window > 0 && hi_any - p.window + 1 > 0 ? hi_any - p.window + 1 : 0;
-
-    // Q^T fragments: step j holds elements g4 * KB + 8 j ...
-    bf16x8 q[D / 32];
-    {
-      const uint16_t* from = p.q + s * p.sq_s + (int64_t)r.qi * p.sq_n + (int64_t)qh * p.sq_h + g4 * KB;
+    // query positions of the wave's rows, and what they see together and each
+    const int wrow0 = row0 + wgroup * MT * 16;
+    const int qi_first = uniform(wrow0 / p.group);
+    const int qi_last = uniform((wrow0 + 16 * MT < p.rows ? wrow0 + 16 * MT - 1 : p.rows - 1) / p.group);
+    const int hi_all = len - p.n + qi_first, hi_any = len - p.n + qi_last;
+    const int lo_any = p.window > 0 && hi_all - p.window + 1 > 0 ? hi_all - p.window + 1 : 0;
+    const int lo_all = p.window > 0 && hi_any - p.window + 1 > 0 ? hi_any - p.window + 1 : 0;
+    Rows r[MT];
+    bf16x8 q[MT][D / 32];  // Q^T fragments: step j holds elements g4 * KB + 8 j ...
+    RowState<D> st[MT];
+#pragma unroll
+    for (int k = 0; k < MT; ++k) {
+      const int row = wrow0 + 16 * k + r16;
+      const bool row_ok = row < p.rows;
+      const int qi = row_ok ? row / p.group : 0, qh = h * p.group + (row_ok ? row - qi * p.group : 0);
+      const int qpos = len - p.n + qi;
+      r[k].see_hi = row_ok ? qpos : -1;
+      r[k].see_lo = p.window > 0 && qpos - p.window + 1 > 0 ? qpos - p.window + 1 : 0;
+      const uint16_t* from = p.q + s * p.sq_s + (int64_t)qi * p.sq_n + (int64_t)qh * p.sq_h + g4 * KB;
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
         i32x4 v = {0, 0, 0, 0};
         if (row_ok) v = *reinterpret_cast<const i32x4*>(from + 8 * j);
-        q[j] = __builtin_bit_cast(bf16x8, v);
+        q[k][j] = __builtin_bit_cast(bf16x8, v);
       }
-    }
-    RowState<D> st;
 #pragma unroll
-    for (int i = 0; i < VB; ++i) st.o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    st.m = -INFINITY;
-    st.l = 0.0f;
+      for (int i = 0; i < VB; ++i) st[k].o[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      st[k].m = -INFINITY;
+      st[k].l = 0.0f;
+    }
 
-    // the piece's tiles that some row of this row tile sees, one stream each in turn
+    // the piece's tiles that some row of the wave sees, one stream each in turn
     int ta = sp.begin + t0, tb = sp.begin + t1;
     const int t_last = hi_any < 0 ? -1 : hi_any / 32;
     if (ta < lo_any / 32) ta = lo_any / 32;
     if (tb > t_last + 1) tb = t_last + 1;  // (none where the queries see nothing: there may be no page to read)
-    if (first_row >= p.rows) tb = ta;
+    if (wrow0 >= p.rows) tb = ta;
     const Heads hd = {p.table + s * p.s_table, p.k_cache + h * p.skc_h, p.v_cache + h * p.svc_h,
                       p.k_scale + h * p.sks_h, p.v_scale + h * p.svs_h, len};
     int t = uniform(ta + stream);
     tb = uniform(tb);
-    TileRef next;
-    find_tile(p, hd, t, t < tb, next);
+    // Pages are looked up two tiles ahead, keys loaded one tile ahead -- into
+    // the registers that the present tile's have just left -- and values
+    // while the scores are formed.
+    Pages ahead;
+    Place place;
+    Tile<D> x;
+    if (t < tb) {
+      find_pages(p, hd, t, true, ahead);
+      place_tile(p, hd, ahead, place);
+      load_k<D>(p, hd, t, place, k_lane, x);
+      find_pages(p, hd, t + streams, t + streams < tb, ahead);
+    }
     while (t < tb) {
-      const TileRef ref = next;
-      Tile<D> x;
-      load_tile<D>(p, hd, t, ref, k_lane, v_lane, x);
-      find_tile(p, hd, t + streams, t + streams < tb, next);  // (its page is known when its turn comes)
-      const bool whole = t * 32 >= r.lo_all && t * 32 + 31 <= r.hi_all && ref.ok[0] && ref.ok[1];
-      const f16x8 pf = weigh<D>(x, ref, q, r, whole, t, g4, qk, st);
-      if (!whole) {
-        clear_values<D>(ref, t, g4, lo_any, hi_any, x);
-        if (r.qi_first != r.qi_last) take_out_nans<D>(ref, r, t, g4, x, st);
+      const Place now = place;
+      load_v<D>(p, hd, t, now, v_lane, x);
+      f32x4 sc[MT][2];
+      scores<D, MT>(x, q, sc);
+      __builtin_amdgcn_sched_barrier(0);
+      if (t + streams < tb) {
+        place_tile(p, hd, ahead, place);
+        load_k<D>(p, hd, t + streams, place, k_lane, x);
+        find_pages(p, hd, t + 2 * streams, t + 2 * streams < tb, ahead);
       }
-      add_values<D>(x, pf, st);
+      __builtin_amdgcn_sched_barrier(0);
+      const bool whole = t * 32 >= lo_all && t * 32 + 31 <= hi_all && now.ok[0] && now.ok[1];
+      f16x8 pf[MT];
+      weigh<D, MT>(sc, now, r, whole, t, g4, qk, st, pf);
+      if (!whole) {
+        clear_values<D>(now, t, g4, lo_any, hi_any, x);
+        if (qi_first != qi_last) take_out_nans<D, MT>(now, r, t, g4, x, st);
+      }
+      add_values<D, MT>(x, pf, st);
       t += streams;
     }
 
-    // join the streams: each scales its output to the common maximum, then
-    // every thread sums four columns of a row
-    st.l += __shfl_xor(st.l, 16, 64);
-    st.l += __shfl_xor(st.l, 32, 64);
+    // join the waves: each scales its output to the common maximum, then every
+    // thread sums four columns of a row
     if (SPLIT) __syncthreads();  // the last piece's join has been read
-    if (g4 == 0) {
-      sm[wave][r16] = st.m;
-      sl[wave][r16] = st.l;
+#pragma unroll
+    for (int k = 0; k < MT; ++k) {
+      st[k].l = quarters(st[k].l, [](float a, float b) { return a + b; });
+      if (g4 == 0) {
+        sm[k][wave][r16] = st[k].m;
+        sl[k][wave][r16] = st[k].l;
+      }
     }
-    __syncthreads();
-    float m = -INFINITY;
-    for (int w = wave % p.rt; w < ATTN_WAVES; w += p.rt) m = fmaxf(m, sm[w][r16]);
-    // (without a maximum the sums are 0, or NaN where every score is NaN)
-    const float f = st.m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st.m - m);
     const bool piece = t0 > 0 || t1 < nt;
     float* part = piece ? part_at<D>(p, 2 * (int64_t)blockIdx.x + (t0 == 0)) : nullptr;
 #pragma unroll
-    for (int c0 = 0; c0 < D; c0 += CW) {
-      if (c0 > 0) __syncthreads();
-      // element (i, e) of the lane is output element g4 * KB + e * VB + i
-      if (g4 * KB >= c0 && g4 * KB < c0 + CW) {
+    for (int k = 0; k < MT; ++k) {
+      if (row0 + 16 * k >= p.rows) break;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+      for (int c0 = 0; c0 < D; c0 += CW) {
+        __syncthreads();
+        // element (i, e) of the lane is output element g4 * KB + e * VB + i
+        if (g4 * KB >= c0 && g4 * KB < c0 + CW) {
+          float m = -INFINITY;
+          for (int w = wgroup; w < ATTN_WAVES; w += p.wr) m = fmaxf(m, sm[k][w][r16]);
+          // (without a maximum the sums are 0, or NaN where every score is NaN)
+          const float f = st[k].m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st[k].m - m);
 #pragma unroll
-          for (int i = 0; i < VB; i += 4)
-            *reinterpret_cast<f32x4*>(&so[wave][r16][g4 * KB - c0 + e * VB + i]) =
-                f32x4{st.o[i][e] * f, st.o[i + 1][e] * f, st.o[i + 2][e] * f, st.o[i + 3][e] * f};
-      }
-      __syncthreads();
-      for (int j = threadIdx.x; j < p.rt * 16 * (CW / 4); j += ATTN_THREADS) {
-        const int c = j % (CW / 4) * 4, rr = j / (CW / 4), tile = rr / 16, rw = rr % 16;
-        if (row0 + rr >= p.rows) continue;
-        f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-        float mm = -INFINITY, ll = 0.0f;
-        for (int w = tile; w < ATTN_WAVES; w += p.rt) {
-          const f32x4 v = *reinterpret_cast<const f32x4*>(&so[w][rw][c]);
+          for (int e = 0; e < 4; ++e)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) o[e] += v[e];
-          mm = fmaxf(mm, sm[w][rw]);
+            for (int i = 0; i < VB; i += 4)
+              *reinterpret_cast<f32x4*>(&so[wave][r16][g4 * KB - c0 + e * VB + i]) =
+                  f32x4{st[k].o[i][e] * f, st[k].o[i + 1][e] * f, st[k].o[i + 2][e] * f, st[k].o[i + 3][e] * f};
         }
-        for (int w = tile; w < ATTN_WAVES; w += p.rt)
-          ll += sl[w][rw] * (sm[w][rw] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(sm[w][rw] - mm));
-        if (SPLIT && piece) {
-          *reinterpret_cast<f32x4*>(part + rr * D + c0 + c) = o;
-          if (c0 + c == 0) {
-            part[p.rt * 16 * D + rr] = mm;
-            part[p.rt * 16 * (D + 1) + rr] = ll;
+        __syncthreads();
+        for (int j = threadIdx.x; j < p.wr * 16 * (CW / 4); j += ATTN_THREADS) {
+          const int c = j % (CW / 4) * 4, rw = j / (CW / 4) % 16, g = j / (CW / 4) / 16, rr = (g * MT + k) * 16 + rw;
+          if (row0 + rr >= p.rows) continue;
+          f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
+          float mm = -INFINITY, ll = 0.0f;
+          for (int w = g; w < ATTN_WAVES; w += p.wr) mm = fmaxf(mm, sm[k][w][rw]);
+          for (int w = g; w < ATTN_WAVES; w += p.wr) {
+            const f32x4 v = *reinterpret_cast<const f32x4*>(&so[w][rw][c]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[e] += v[e];
+            ll += sl[k][w][rw] * (sm[k][w][rw] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(sm[k][w][rw] - mm));
           }
-        } else {
-          store_row<D>(p, s, h, row0 + rr, c0 + c, o, mm, ll);
+          if (SPLIT && piece) {
+            *reinterpret_cast<f32x4*>(part + rr * D + c0 + c) = o;
+            if (c0 + c == 0) {
+              part[p.rt * 16 * D + rr] = mm;
+              part[p.rt * 16 * (D + 1) + rr] = ll;
+            }
+          } else {
+            store_row<D>(p, s, h, row0 + rr, c0 + c, o, mm, ll);
+          }
         }
       }
     }
@@ -578,9 +654,9 @@ __global__ __launch_bounds__(ATTN_THREADS, D > 128 ? 2 : 3) void paged_attention
     if (t0 == 0 && threadIdx.x == 0) {
       int32_t* parts = unit_parts(p, (int64_t)s * p.units + unit);
       parts[0] = blockIdx.x;
-      parts[1] = (int32_t)((at + nt - 1) / share);
+      parts[1] = (line.at + nt - 1) / line.size;
     }
-    at += t1 - t0;
+    line.at += t1 - t0;
   }
 }
 
@@ -652,37 +728,42 @@ __global__ __launch_bounds__(ATTN_THREADS) void paged_attention_join_kernel(cons
 
 // What is launched: a pure function of the sizes.
 struct AttnPlan {
-  int rt, units;        // row tiles a workgroup takes together; (KV head, group of row tiles) per sequence
+  int mt, wr, rt;       // row tiles of a wave, waves side by side, row tiles of a unit
+  int units;            // units (KV head, group of row tiles) per sequence
   bool split;
   int64_t shares;       // workgroups of the first kernel when split
   int min_share;        // tiles of a share at least
   int rps;              // rows per workgroup of the join
 };
 
-// Caches of at most this many tiles (1024 tokens) are not cut: the cut costs
-// two scans of the lengths and the join's launch, together about 7 us, and a
-// workgroup goes through 1024 tokens of a head of 128 in 12.6 us.
-constexpr int64_t DIRECT_TILES = 32;
-// Parts of one call: at most 40 MiB.
-constexpr int64_t WORKSPACE_FLOATS = 10 << 20;
-
-// Shares: as many as are resident at once on 256 compute units (registers:
-// four workgroups a unit at D = 64, three at 128, two at 256), so that all
-// end together.  At D = 128 512 / 768 / 1024 shares took 223 / 219 / 227 us
-// (128 sequences up to 8192 long, 8 heads) and 80 / 82 / 85 us (4 sequences
-// up to 131071 long, 4 heads); at D = 256 512 / 635 took 34 / 45 us.
-int64_t most_shares(int64_t D) { return D == 64 ? 1024 : D == 128 ? 768 : 512; }
-
 AttnPlan attn_plan(int64_t S, int64_t Hkv, int64_t row_tiles, int64_t D, int64_t cap) {
   AttnPlan a;
-  a.rt = row_tiles >= 3 ? 4 : (int)row_tiles;
+  // two row tiles a wave where its registers (output and queries: D MT 3 / 8
+  // a lane) leave room for two waves a SIMD
+  a.mt = row_tiles >= 2 && D <= 128 ? 2 : 1;
+  const int64_t groups = (row_tiles + a.mt - 1) / a.mt;
+  a.wr = groups >= 3 ? 4 : groups == 2 ? 2 : 1;
+  a.rt = a.mt * a.wr;
   a.units = (int)(Hkv * ((row_tiles + a.rt - 1) / a.rt));
   const int64_t cap_tiles = (cap + 31) / 32, units = S * a.units;
-  a.split = cap_tiles > DIRECT_TILES;
-  a.min_share = ATTN_WAVES / a.rt;  // a tile for each stream
-  const int64_t part = a.rt * 16 * (D + 2);
-  int64_t most = WORKSPACE_FLOATS / (2 * part);
-  if (most > most_shares(D)) most = most_shares(D);
+  // Short caches are not cut, the longer the more units there are to fill the
+  // machine: the cut costs the scans of the lengths and the join's launch, about
+  // 7 us.  Not cut / cut, in us (cache capacity; lengths from half of it up):
+  // 8 units of D = 128: 1024 tokens 10.5 / 11.5, 2048 tokens 16.4 / 11.8;
+  // 128 units: 2048 tokens 19.7 / 22.8, 4096 tokens 35.0 / 30.3;
+  // 512 units: 2048 tokens 42.8 / 54.0, 4096 tokens 78.5 / 90.3;
+  // 1024 units of lengths from 1 to 8192: 279 / 217.
+  const int64_t direct = 32 + units / 4;
+  a.split = cap_tiles > (direct < 128 ? direct : 128);
+  a.min_share = ATTN_WAVES / a.wr;  // a tile for each stream
+  // Shares: as many workgroups as are resident at once on 256 compute units,
+  // so that all end together.  At D = 128 512 / 768 / 1024 shares took 223 /
+  // 219 / 227 us (128 sequences up to 8192 long, 8 heads) and 80 / 82 / 85 us
+  // (4 sequences up to 131071 long, 4 heads).
+  int64_t most = 256 * WAVES_PER_SIMD((int)D, a.mt);
+  // (and the parts of one call within 40 MiB)
+  const int64_t fit = (int64_t(10) << 20) / (2 * a.rt * 16 * (D + 2));
+  if (most > fit) most = fit;
   const int64_t want = (units * cap_tiles + a.min_share - 1) / a.min_share;
   a.shares = want < most ? want : most;
   // few units: a row to a workgroup; many: as many rows as its threads hold
@@ -695,13 +776,14 @@ AttnPlan attn_plan(int64_t S, int64_t Hkv, int64_t row_tiles, int64_t D, int64_t
 // Workgroups of the join.
 int64_t join_grid(const AttnPlan& a, int64_t S) { return S * a.units * (a.rt * 16 / a.rps); }
 
-template <int D>
+template <int D, int MT>
 hipError_t launch(const PagedAttnArgs& p, const AttnPlan& a, hipStream_t stream) {
   if (!a.split) {
-    paged_attention_kernel<D, false><<<dim3((unsigned)((int64_t)p.S * p.units)), dim3(ATTN_THREADS), 0, stream>>>(p);
+    paged_attention_kernel<D, MT, false>
+        <<<dim3((unsigned)((int64_t)p.S * p.units)), dim3(ATTN_THREADS), 0, stream>>>(p);
     return hipGetLastError();
   }
-  paged_attention_kernel<D, true><<<dim3((unsigned)p.shares), dim3(ATTN_THREADS), 0, stream>>>(p);
+  paged_attention_kernel<D, MT, true><<<dim3((unsigned)p.shares), dim3(ATTN_THREADS), 0, stream>>>(p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   paged_attention_join_kernel<D><<<dim3((unsigned)join_grid(a, p.S)), dim3(ATTN_THREADS), 0, stream>>>(p);
@@ -723,15 +805,20 @@ int64_t paged_attention_grid(int64_t S, int64_t Hkv, int64_t row_tiles, int64_t 
 hipError_t launch_paged_attention(PagedAttnArgs p, hipStream_t stream) {
   const AttnPlan a = attn_plan(p.S, p.Hkv, p.row_tiles, p.D, (int64_t)p.max_pages * p.P);
   p.rt = a.rt;
+  p.wr = a.wr;
   p.units = a.units;
   p.groups = a.units / p.Hkv;
   p.shares = (int32_t)a.shares;
   p.min_share = a.min_share;
   p.rps = a.rps;
   p.log_p = __builtin_ctz(p.P);
-  if (p.D == 64) return launch<64>(p, a, stream);
-  if (p.D == 128) return launch<128>(p, a, stream);
-  return launch<256>(p, a, stream);
+#define ATTN_CASE(D_, MT) \
+  if (p.D == D_ && a.mt == MT) return launch<D_, MT>(p, a, stream);
+  ATTN_CASE(64, 1) ATTN_CASE(64, 2)
+  ATTN_CASE(128, 1) ATTN_CASE(128, 2)
+  ATTN_CASE(256, 1)
+#undef ATTN_CASE
+  return hipErrorInvalidValue;
 }
 
 }  // namespace dgmi

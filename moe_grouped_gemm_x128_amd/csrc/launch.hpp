@@ -154,19 +154,22 @@ struct PagedAttnArgs {
   float* lse;
   int64_t sl_s, sl_n, sl_h;
   const uint8_t *k_cache, *v_cache;
-  int64_t skc_p, skc_h, skc_t, svc_p, svc_h, svc_t;
+  int64_t skc_h, svc_h;
+  uint32_t skc_p, skc_t, svc_p, svc_t;
   const float *k_scale, *v_scale;
-  int64_t sks_p, sks_h, svs_p, svs_h;
+  int64_t sks_h, svs_h;
+  uint32_t sks_p, svs_p;  // bytes
   const int32_t* table;
   int64_t s_table;
   const int32_t* lens;
   int32_t S, n, Hkv, group, rows, row_tiles, D, P, max_pages, pages, window;
   float scale;
   float* workspace;
-  // set by the launcher: row tiles a workgroup takes together, units (KV head,
+  // set by the launcher: row tiles of a unit, waves that take
+  // them side by side, units (KV head,
   // group of row tiles) per sequence, groups per head, workgroups of the first kernel, tiles a
   // workgroup takes at least, rows per workgroup of the join, log2 P
-  int32_t rt, units, groups, shares, min_share, rps, log_p;
+  int32_t rt, wr, units, groups, shares, min_share, rps, log_p;
 };
 
 struct PackArgs {

@@ -138,6 +138,39 @@ def test_long_caches(D, P, S, H, group, lens):
     _compare(c, out, lse, D ** -0.5, 0, "long")
 
 
+@pytest.mark.parametrize("D,P,S,n,H,group,window,lens", [
+    (64, 16, 2, 6, 1, 20, 0, [4500, 77]),       # 120 rows: four row tiles a wave, two waves side by side
+    (64, 64, 2, 1, 2, 30, 0, [5000, 4999]),     # two row tiles
+    (128, 32, 2, 5, 1, 16, 1000, [6000, 1030]), # 80 rows, a window
+    (128, 64, 1, 4, 2, 8, 0, [7001]),
+    (128, 16, 1, 7, 1, 25, 0, [4300]),          # 175 rows: more than one workgroup's
+    (256, 64, 2, 4, 1, 8, 0, [4400, 9]),
+    (256, 16, 1, 3, 1, 33, 333, [5123]),        # 99 rows
+])
+def test_long_caches_with_many_rows(D, P, S, n, H, group, window, lens):
+    say(f"paged_attention_fp8 long, many rows D={D} P={P} n={n} group={group} window={window} lens={lens}")
+    c = _case(D + n, S, n, H * group, H, D, P, lens)
+    out, lse = _run(c, D ** -0.5, window)
+    _compare(c, out, lse, D ** -0.5, window, "long, many rows")
+
+
+def test_more_sequences_than_threads():
+    """Six hundred sequences, most of them short or empty, in a table wide
+    enough for the work to be cut along the cache; and without a cut."""
+    say("paged_attention_fp8 600 sequences")
+    rng = np.random.default_rng(77)
+    lens = [int(v) for v in rng.integers(0, 40, size=600)]
+    lens[3], lens[255], lens[256], lens[511], lens[599] = 2500, 700, 0, 33, 900
+    c = _case(81, 600, 1, 2, 1, 64, 16, lens)
+    out, lse = _run(c, 0.125)
+    _compare(c, out, lse, 0.125, 0, "600 sequences, not cut")
+    wide = np.full((600, 300), -1, dtype=np.int32)
+    wide[:, :c["table"].shape[1]] = c["table"]
+    c["table"] = wide
+    out, lse = _run(c, 0.125)
+    _compare(c, out, lse, 0.125, 0, "600 sequences, cut")
+
+
 def test_sharp_scores():
     """Scores of several hundred: one token takes all the weight, the
     running maximum moves along the cache."""

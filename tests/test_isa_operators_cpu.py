@@ -11,7 +11,7 @@ import pytest
 from test_isa_cpu import BUILD, LLVM, _extract
 
 
-@pytest.mark.parametrize("src,kernels", [("route.hip", 25), ("kvcache.hip", 6), ("attn.hip", 9)])
+@pytest.mark.parametrize("src,kernels", [("route.hip", 25), ("kvcache.hip", 18), ("attn.hip", 13)])
 def test_no_spills_and_no_packed_fp32(src, kernels, tmp_path):
     co = _extract(os.path.join(BUILD, src + ".o"), tmp_path)
     notes = subprocess.run([os.path.join(LLVM, "llvm-readelf"), "--notes", co], check=True, capture_output=True,
