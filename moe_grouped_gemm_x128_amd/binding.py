@@ -161,10 +161,9 @@ def _dtype_code(t):
     return code
 
 
-# a dg_tensor as bytes: data, dtype, ndim, shape[4], stride[4]
-_PACK = struct.Struct("@Qii4q4q")
-_PAD = ((), (0, 0, 0), (0, 0), (0,), ())
-assert _PACK.size == ctypes.sizeof(DgTensor)
+# a dg_tensor as bytes, by rank: data, dtype, ndim, shape[4], stride[4], what
+# the rank leaves over zero
+_PACK = (None,) + tuple(struct.Struct(f"@Qii{n}q{32 - 8 * n}x{n}q{32 - 8 * n}x").pack for n in range(1, 5))
 
 
 def _packed(t, dtype=None):
@@ -174,9 +173,11 @@ def _packed(t, dtype=None):
     n = len(shape)
     if n < 1 or n > 4:
         raise ValueError("dg_tensor supports 1 to 4 dims")
-    code = _dtype_code(t) if dtype is None else dtype
-    pad = _PAD[n]
-    return _PACK.pack(t.data_ptr(), code, n, *shape, *pad, *t.stride(), *pad)
+    if dtype is None:
+        dtype = _DTYPE_CODES.get(t.dtype)
+        if dtype is None:
+            dtype = _dtype_code(t)
+    return _PACK[n](t.data_ptr(), dtype, n, *shape, *t.stride())
 
 
 def describe(t, dtype=None):
