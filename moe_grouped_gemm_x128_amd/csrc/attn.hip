@@ -189,28 +189,26 @@ __device__ __forceinline__ void find_pages(const PagedAttnArgs& p, const Heads& 
   if (p.P == 16 && wanted && t * 32 + 16 < hd.len) x.id1 = uniform_load(hd.table + 2 * t + 1);
 }
 
-// Where a tile's halves are, and their scales (1 where a half takes no part:
-// its page is outside the pool, and page 0 is read instead).
-struct Place {
-  int page[2];
-  float ks[2], vs[2];
-  bool ok[2];
-};
+// Half u's page; page 0 is read where it takes no part (ok: it does).
+__device__ __forceinline__ int page_of(const PagedAttnArgs& p, const Pages& x, int u, bool* ok) {
+  const int id = u == 0 || p.P > 16 ? x.id0 : x.id1;
+  *ok = id >= 0 && id < p.pages;
+  return *ok ? id : 0;
+}
 // One page's place: strides are below 2^32 bytes, a page's tokens within 2^31.
 __device__ __forceinline__ uint64_t page_offset(int page, uint32_t stride) { return (uint64_t)(uint32_t)page * stride; }
 
-__device__ __forceinline__ float page_scale(const float* base, int page, uint32_t stride, bool ok) {
-  const int v = uniform_load(reinterpret_cast<const int32_t*>(reinterpret_cast<const uint8_t*>(base) + page_offset(page, stride)));
-  return __int_as_float(ok ? v : 0x3f800000);
-}
-__device__ __forceinline__ void place_tile(const PagedAttnArgs& p, const Heads& hd, const Pages& pages, Place& x) {
+// The scales of a tile's halves as they are stored.
+struct Scales {
+  int ks[2], vs[2];
+  bool ok[2];
+};
+__device__ __forceinline__ void load_scales(const PagedAttnArgs& p, const Heads& hd, const Pages& pages, Scales& x) {
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const int id = u == 0 || p.P > 16 ? pages.id0 : pages.id1;
-    x.ok[u] = id >= 0 && id < p.pages;
-    x.page[u] = x.ok[u] ? id : 0;
-    x.ks[u] = page_scale(hd.ks, x.page[u], p.sks_p, x.ok[u]);
-    x.vs[u] = page_scale(hd.vs, x.page[u], p.svs_p, x.ok[u]);
+    const int page = page_of(p, pages, u, &x.ok[u]);
+    x.ks[u] = uniform_load(reinterpret_cast<const int32_t*>(reinterpret_cast<const uint8_t*>(hd.ks) + page_offset(page, p.sks_p)));
+    x.vs[u] = uniform_load(reinterpret_cast<const int32_t*>(reinterpret_cast<const uint8_t*>(hd.vs) + page_offset(page, p.svs_p)));
   }
 }
 
@@ -224,13 +222,14 @@ struct Tile {
 // lane: this lane's offset inside a 16-token half.  (Kept opaque, so that the
 // loads take a scalar base and a 32-bit offset.)
 template <int D>
-__device__ __forceinline__ void load_k(const PagedAttnArgs& p, const Heads& hd, int t, const Place& at, uint32_t lane,
+__device__ __forceinline__ void load_k(const PagedAttnArgs& p, const Heads& hd, int t, const Pages& pages, uint32_t lane,
                                        Tile<D>& x) {
   asm volatile("" : "+v"(lane));
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int slot = (t * 32 + 16 * u) & (p.P - 1);
-    const uint8_t* kp = hd.k + page_offset(at.page[u], p.skc_p) + slot * p.skc_t;
+    bool ok;
+    const uint8_t* kp = hd.k + page_offset(page_of(p, pages, u, &ok), p.skc_p) + slot * p.skc_t;
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
       const i32x4 v = *reinterpret_cast<const i32x4*>(kp + lane + 16 * j);
@@ -241,7 +240,7 @@ __device__ __forceinline__ void load_k(const PagedAttnArgs& p, const Heads& hd, 
 }
 
 template <int D>
-__device__ __forceinline__ void load_v(const PagedAttnArgs& p, const Heads& hd, int t, const Place& at, uint32_t lane,
+__device__ __forceinline__ void load_v(const PagedAttnArgs& p, const Heads& hd, int t, const Pages& pages, uint32_t lane,
                                        Tile<D>& x) {
   constexpr int VB = D / 16;
   uint32_t off[4];
@@ -253,7 +252,8 @@ __device__ __forceinline__ void load_v(const PagedAttnArgs& p, const Heads& hd, 
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const int slot = (t * 32 + 16 * u) & (p.P - 1);
-    const uint8_t* vp = hd.v + page_offset(at.page[u], p.svc_p) + slot * p.svc_t;
+    bool ok;
+    const uint8_t* vp = hd.v + page_offset(page_of(p, pages, u, &ok), p.svc_p) + slot * p.svc_t;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint8_t* row = vp + off[e];
@@ -316,19 +316,21 @@ __device__ __forceinline__ void scores(const Tile<D>& x, const bf16x8 (&q)[MT][D
 // are scaled to the new maxima; pf gets P^T as the second product wants it.
 // whole: every row sees all 32 positions.
 template <int D, int MT>
-__device__ __forceinline__ void weigh(const f32x4 (&sc)[MT][2], const Place& x, const Rows (&r)[MT], bool whole, int t,
+__device__ __forceinline__ void weigh(const f32x4 (&sc)[MT][2], const Scales& x, const Rows (&r)[MT], bool whole, int t,
                                       int g4, float qk, RowState<D> (&st)[MT], f16x8 (&pf)[MT]) {
-  float lsv[2], inv[2];
+  float c[2], lsv[2], inv[2];  // (scales count as 1 where a half takes no part: page 0's may be anything)
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    lsv[u] = __builtin_amdgcn_logf(x.vs[u]);
-    inv[u] = __builtin_amdgcn_rcpf(x.vs[u]);
+    const float vs = __int_as_float(x.ok[u] ? x.vs[u] : 0x3f800000);
+    c[u] = __int_as_float(x.ok[u] ? x.ks[u] : 0x3f800000) * qk;
+    lsv[u] = __builtin_amdgcn_logf(vs);
+    inv[u] = __builtin_amdgcn_rcpf(vs);
   }
 #pragma unroll
   for (int k = 0; k < MT; ++k) {
     float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __builtin_fmaf(sc[k][i / 4][i % 4], x.ks[i / 4] * qk, lsv[i / 4]);
+    for (int i = 0; i < 8; ++i) y[i] = __builtin_fmaf(sc[k][i / 4][i % 4], c[i / 4], lsv[i / 4]);
     if (!whole) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -394,7 +396,7 @@ __device__ __forceinline__ void add_values(const Tile<D>& x, const f16x8 (&pf)[M
 // Clears the values of positions outside [lo, hi] and of absent pages: their
 // codes may be NaN, and a weight of 0 would not hide that.
 template <int D>
-__device__ __forceinline__ void clear_values(const Place& place, int t, int g4, int lo, int hi, Tile<D>& x) {
+__device__ __forceinline__ void clear_values(const Scales& place, int t, int g4, int lo, int hi, Tile<D>& x) {
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int at = t * 32 + 16 * (i / 4) + 4 * g4 + i % 4;
@@ -409,7 +411,7 @@ __device__ __forceinline__ void clear_values(const Place& place, int t, int g4, 
 // weight of 0 times NaN is NaN.  The NaN codes are cleared, and a product of
 // their places with what each row sees says which outputs they make NaN.
 template <int D, int MT>
-__device__ __forceinline__ void take_out_nans(const Place& place, const Rows (&r)[MT], int t, int g4, Tile<D>& x,
+__device__ __forceinline__ void take_out_nans(const Scales& place, const Rows (&r)[MT], int t, int g4, Tile<D>& x,
                                               RowState<D> (&st)[MT]) {
   Tile<D> places;  // code 1 (a positive value) where there is a NaN
   int hit = 0;
@@ -561,35 +563,33 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
     // Pages are looked up two tiles ahead, keys loaded one tile ahead -- into
     // the registers that the present tile's have just left -- and values
     // while the scores are formed.
-    Pages ahead;
-    Place place;
+    Pages now, next, ahead;
     Tile<D> x;
     if (t < tb) {
-      find_pages(p, hd, t, true, ahead);
-      place_tile(p, hd, ahead, place);
-      load_k<D>(p, hd, t, place, k_lane, x);
-      find_pages(p, hd, t + streams, t + streams < tb, ahead);
+      find_pages(p, hd, t, true, now);
+      find_pages(p, hd, t + streams, t + streams < tb, next);
+      load_k<D>(p, hd, t, now, k_lane, x);
     }
     while (t < tb) {
-      const Place now = place;
+      Scales scl;
+      load_scales(p, hd, now, scl);
+      find_pages(p, hd, t + 2 * streams, t + 2 * streams < tb, ahead);
       load_v<D>(p, hd, t, now, v_lane, x);
       f32x4 sc[MT][2];
       scores<D, MT>(x, q, sc);
       __builtin_amdgcn_sched_barrier(0);
-      if (t + streams < tb) {
-        place_tile(p, hd, ahead, place);
-        load_k<D>(p, hd, t + streams, place, k_lane, x);
-        find_pages(p, hd, t + 2 * streams, t + 2 * streams < tb, ahead);
-      }
+      if (t + streams < tb) load_k<D>(p, hd, t + streams, next, k_lane, x);
       __builtin_amdgcn_sched_barrier(0);
-      const bool whole = t * 32 >= lo_all && t * 32 + 31 <= hi_all && now.ok[0] && now.ok[1];
+      const bool whole = t * 32 >= lo_all && t * 32 + 31 <= hi_all && scl.ok[0] && scl.ok[1];
       f16x8 pf[MT];
-      weigh<D, MT>(sc, now, r, whole, t, g4, qk, st, pf);
+      weigh<D, MT>(sc, scl, r, whole, t, g4, qk, st, pf);
       if (!whole) {
-        clear_values<D>(now, t, g4, lo_any, hi_any, x);
-        if (qi_first != qi_last) take_out_nans<D, MT>(now, r, t, g4, x, st);
+        clear_values<D>(scl, t, g4, lo_any, hi_any, x);
+        if (qi_first != qi_last) take_out_nans<D, MT>(scl, r, t, g4, x, st);
       }
       add_values<D, MT>(x, pf, st);
+      now = next;
+      next = ahead;
       t += streams;
     }
 
