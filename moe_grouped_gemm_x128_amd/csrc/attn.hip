@@ -25,9 +25,10 @@
 // E4M3 is exact in BF16 and in FP16.  Keys meet the BF16 queries in BF16.
 // The weights P are rounded to FP16 (11 bits; rounding them to BF16 would add
 // as much error again as the BF16 output has); to keep them in FP16's range
-// the scale of V is taken into the exponent: with y_t = x_t log2 e + log2 sv,
-//   o = sum_t 2^(y_t - M) code_t / sum_t 2^(y_t - M) / sv,  M = max y,
-// shifted by 2^14, so that weights down to 2^-28 of the largest are normal.
+// the scale of V is taken into the exponent: with y_t = x_t log2 e + log2 sv_t,
+//   o = sum_t 2^(y_t - M) code_t / sum_t 2^(y_t - M) / sv_t,  M = max y,
+// and P is held times 2^14, so that weights down to 2^-28 of the largest are
+// normal numbers.
 // Sums, maxima and the output stay in FP32.
 //
 // Work is cut along the cache by device-side lengths: the 32-token tiles of
@@ -54,7 +55,7 @@ constexpr int ATTN_THREADS = 64 * ATTN_WAVES;
 // Waves per SIMD that the registers are held to: the output takes D / 4 MT
 // registers of a lane, the queries D / 8 MT, a tile's codes D / 4.
 constexpr int WAVES_PER_SIMD(int D, int MT) { return D * MT <= 128 ? 3 : 2; }
-constexpr float P_SHIFT = 14.0f;  // weights are held times 2^14
+constexpr float P_GAIN = 16384.0f;  // weights are held times 2^14 in FP16
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
 
 // Four E4M3 codes -> four BF16 values in two words.
@@ -219,9 +220,17 @@ struct Tile {
   int v[2][4][D / 64];  // D / 16 bytes of four tokens in each half
 };
 
+// ONCE: no other wave reads these codes and no cache will hold them until the
+// next call, so they are loaded past the caches (non-temporal).
+template <bool ONCE, typename T>
+__device__ __forceinline__ T load_codes(const uint8_t* at) {
+  if constexpr (ONCE) return __builtin_nontemporal_load(reinterpret_cast<const T*>(at));
+  else return *reinterpret_cast<const T*>(at);
+}
+
 // lane: this lane's offset inside a 16-token half.  (Kept opaque, so that the
 // loads take a scalar base and a 32-bit offset.)
-template <int D>
+template <int D, bool ONCE>
 __device__ __forceinline__ void load_k(const PagedAttnArgs& p, const Heads& hd, int t, const Pages& pages, uint32_t lane,
                                        Tile<D>& x) {
   asm volatile("" : "+v"(lane));
@@ -232,14 +241,14 @@ __device__ __forceinline__ void load_k(const PagedAttnArgs& p, const Heads& hd, 
     const uint8_t* kp = hd.k + page_offset(page_of(p, pages, u, &ok), p.skc_p) + slot * p.skc_t;
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
-      const i32x4 v = *reinterpret_cast<const i32x4*>(kp + lane + 16 * j);
+      const i32x4 v = load_codes<ONCE, i32x4>(kp + lane + 16 * j);
 #pragma unroll
       for (int e = 0; e < 4; ++e) x.k[u][4 * j + e] = v[e];
     }
   }
 }
 
-template <int D>
+template <int D, bool ONCE>
 __device__ __forceinline__ void load_v(const PagedAttnArgs& p, const Heads& hd, int t, const Pages& pages, uint32_t lane,
                                        Tile<D>& x) {
   constexpr int VB = D / 16;
@@ -258,13 +267,13 @@ __device__ __forceinline__ void load_v(const PagedAttnArgs& p, const Heads& hd, 
     for (int e = 0; e < 4; ++e) {
       const uint8_t* row = vp + off[e];
       if constexpr (VB == 4) {
-        x.v[u][e][0] = *reinterpret_cast<const int*>(row);
+        x.v[u][e][0] = load_codes<ONCE, int>(row);
       } else if constexpr (VB == 8) {
-        const i32x2 v = *reinterpret_cast<const i32x2*>(row);
+        const i32x2 v = load_codes<ONCE, i32x2>(row);
         x.v[u][e][0] = v[0];
         x.v[u][e][1] = v[1];
       } else {
-        const i32x4 v = *reinterpret_cast<const i32x4*>(row);
+        const i32x4 v = load_codes<ONCE, i32x4>(row);
 #pragma unroll
         for (int b = 0; b < 4; ++b) x.v[u][e][b] = v[b];
       }
@@ -330,7 +339,7 @@ __device__ __forceinline__ void weigh(const f32x4 (&sc)[MT][2], const Scales& x,
   for (int k = 0; k < MT; ++k) {
     float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = __builtin_fmaf(sc[k][i / 4][i % 4], c[i / 4], lsv[i / 4]);
+    for (int i = 0; i < 8; ++i) y[i] = sc[k][i / 4][i % 4] * c[i / 4];
     if (!whole) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -338,14 +347,13 @@ __device__ __forceinline__ void weigh(const f32x4 (&sc)[MT][2], const Scales& x,
         y[i] = x.ok[i / 4] && at >= r[k].see_lo && at <= r[k].see_hi ? y[i] : -INFINITY;
       }
     }
-    float mx = y[0];
-#pragma unroll
-    for (int i = 1; i < 8; ++i) mx = fmaxf(mx, y[i]);
+    float mx = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) + lsv[0],
+                     fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])) + lsv[1]);
     mx = quarters(mx, [](float a, float b) { return fmaxf(a, b); });
     const float m_new = fmaxf(st[k].m, mx);
-    const float m_use = m_new == -INFINITY ? 0.0f : m_new - P_SHIFT;  // nothing seen so far
+    const float m_use = m_new == -INFINITY ? 0.0f : m_new;  // nothing seen so far
     if (__any(m_new != st[k].m)) {  // (seldom, once the largest scores have been seen)
-      const float alpha = __builtin_amdgcn_exp2f(st[k].m - P_SHIFT - m_use);
+      const float alpha = __builtin_amdgcn_exp2f(st[k].m - m_use);
       st[k].m = m_new;
       st[k].l *= alpha;
 #pragma unroll
@@ -353,11 +361,14 @@ __device__ __forceinline__ void weigh(const f32x4 (&sc)[MT][2], const Scales& x,
 #pragma unroll
         for (int e = 0; e < 4; ++e) st[k].o[i][e] *= alpha;
     }
+    // (log2 sv - M is exact where it matters, near the largest weight, so that
+    // a weight and the sum are as exact as the score)
+    const float d[2] = {lsv[0] - m_use, lsv[1] - m_use};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float w = __builtin_amdgcn_exp2f(y[i] - m_use);
+      const float w = __builtin_amdgcn_exp2f(y[i] + d[i / 4]);
       st[k].l = __builtin_fmaf(w, inv[i / 4], st[k].l);
-      pf[k][i] = (_Float16)w;
+      pf[k][i] = (_Float16)(w * P_GAIN);
     }
   }
 }
@@ -465,21 +476,24 @@ __device__ __forceinline__ int32_t* unit_parts(const PagedAttnArgs& p, int64_t u
 
 template <int D>
 __device__ __forceinline__ void store_row(const PagedAttnArgs& p, int s, int h, int row, int c4, f32x4 o, float m, float l) {
-  const float inv_l = l != 0.0f ? __fdiv_rn(1.0f, l) : 0.0f;  // (NaN stays NaN)
+  const float inv_l = l != 0.0f ? __fdiv_rn(1.0f / P_GAIN, l) : 0.0f;  // (NaN stays NaN)
 #pragma unroll
   for (int e = 0; e < 4; ++e) o[e] = l != 0.0f ? o[e] * inv_l : 0.0f;
   const int qi = row / p.group, qh = h * p.group + row % p.group;
   *reinterpret_cast<i32x2*>(p.out + s * p.so_s + (int64_t)qi * p.so_n + (int64_t)qh * p.so_h + c4) = to_bf16x4_bits(o);
   if (c4 == 0 && p.lse != nullptr)
+    // log2 l = exponent + log2 of the mantissa: M plus the exponent is small
+    // and exact, the scales of V cancel in it
     p.lse[s * p.sl_s + (int64_t)qi * p.sl_n + (int64_t)qh * p.sl_h] =
-        l != 0.0f ? (m - P_SHIFT + __builtin_amdgcn_logf(l)) * LN2 : -INFINITY;
+        l != 0.0f ? (m + (float)__builtin_amdgcn_frexp_expf(l) + __builtin_amdgcn_logf(__builtin_amdgcn_frexp_mantf(l))) * LN2
+                  : -INFINITY;
 }
 
 // MT: row tiles of a wave: the codes are converted once for up to 16 MT rows.
 // A unit with more rows has them spread over wr waves side by side (the second
 // and later ones find the codes in the caches); the ATTN_WAVES / wr streams of
 // waves take the tiles in turn.
-template <int D, int MT, bool SPLIT>
+template <int D, int MT, bool SPLIT, bool ONCE>
 __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_attention_kernel(const PagedAttnArgs p) {
   constexpr int KB = D / 4;    // bytes of a key per lane
   constexpr int VB = D / 16;   // bytes of a value per lane, and output tiles
@@ -568,17 +582,17 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
     if (t < tb) {
       find_pages(p, hd, t, true, now);
       find_pages(p, hd, t + streams, t + streams < tb, next);
-      load_k<D>(p, hd, t, now, k_lane, x);
+      load_k<D, ONCE>(p, hd, t, now, k_lane, x);
     }
     while (t < tb) {
       Scales scl;
       load_scales(p, hd, now, scl);
       find_pages(p, hd, t + 2 * streams, t + 2 * streams < tb, ahead);
-      load_v<D>(p, hd, t, now, v_lane, x);
+      load_v<D, ONCE>(p, hd, t, now, v_lane, x);
       f32x4 sc[MT][2];
       scores<D, MT>(x, q, sc);
       __builtin_amdgcn_sched_barrier(0);
-      if (t + streams < tb) load_k<D>(p, hd, t + streams, next, k_lane, x);
+      if (t + streams < tb) load_k<D, ONCE>(p, hd, t + streams, next, k_lane, x);
       __builtin_amdgcn_sched_barrier(0);
       const bool whole = t * 32 >= lo_all && t * 32 + 31 <= hi_all && scl.ok[0] && scl.ok[1];
       f16x8 pf[MT];
@@ -776,14 +790,14 @@ AttnPlan attn_plan(int64_t S, int64_t Hkv, int64_t row_tiles, int64_t D, int64_t
 // Workgroups of the join.
 int64_t join_grid(const AttnPlan& a, int64_t S) { return S * a.units * (a.rt * 16 / a.rps); }
 
-template <int D, int MT>
+template <int D, int MT, bool ONCE>
 hipError_t launch(const PagedAttnArgs& p, const AttnPlan& a, hipStream_t stream) {
   if (!a.split) {
-    paged_attention_kernel<D, MT, false>
+    paged_attention_kernel<D, MT, false, ONCE>
         <<<dim3((unsigned)((int64_t)p.S * p.units)), dim3(ATTN_THREADS), 0, stream>>>(p);
     return hipGetLastError();
   }
-  paged_attention_kernel<D, MT, true><<<dim3((unsigned)p.shares), dim3(ATTN_THREADS), 0, stream>>>(p);
+  paged_attention_kernel<D, MT, true, ONCE><<<dim3((unsigned)p.shares), dim3(ATTN_THREADS), 0, stream>>>(p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   paged_attention_join_kernel<D><<<dim3((unsigned)join_grid(a, p.S)), dim3(ATTN_THREADS), 0, stream>>>(p);
@@ -812,8 +826,16 @@ hipError_t launch_paged_attention(PagedAttnArgs p, hipStream_t stream) {
   p.min_share = a.min_share;
   p.rps = a.rps;
   p.log_p = __builtin_ctz(p.P);
-#define ATTN_CASE(D_, MT) \
-  if (p.D == D_ && a.mt == MT) return launch<D_, MT>(p, a, stream);
+  // Past the caches where no waves share codes and the sequences can hold more
+  // than the 256 MiB that the last-level cache keeps from call to call.  With /
+  // without, at D = 128: 128 sequences up to 8192 long (2 GiB at most) 198 / 211
+  // us, 4 up to 131071 long 71 / 81 us, 64 of 1024 to 2048 39.7 / 43.4 us, of
+  // 512 to 1024 (128 MiB) 22.7 / 20.8 us; with codes shared by two waves 44 / 33 us.
+  const bool once = a.rt == a.mt && p.groups == 1 &&
+                    2 * (int64_t)p.S * p.Hkv * p.max_pages * p.P * p.D >= (int64_t(256) << 20);
+#define ATTN_CASE(D_, MT)                              \
+  if (p.D == D_ && a.mt == MT)                         \
+    return once ? launch<D_, MT, true>(p, a, stream) : launch<D_, MT, false>(p, a, stream);
   ATTN_CASE(64, 1) ATTN_CASE(64, 2)
   ATTN_CASE(128, 1) ATTN_CASE(128, 2)
   ATTN_CASE(256, 1)
