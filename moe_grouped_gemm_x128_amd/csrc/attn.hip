@@ -20,8 +20,9 @@
 //     lane takes tokens 4 (l / 16) + {0..3} of two tiles, reads D / 16
 //     consecutive bytes of each, and turns the 8 x D/16 bytes round in its
 //     own registers (one byte permute and two conversions per four codes);
-//   - the head's elements are free in the first product: a lane reads D / 4
-//     consecutive bytes of a token's key.
+//   - the head's elements are free in the first product: a lane reads 16
+//     consecutive bytes of every 64 of a token's key, so that a load takes
+//     whole 64-byte pieces.
 // E4M3 is exact in BF16 and in FP16.  Keys meet the BF16 queries in BF16.
 // The weights P are rounded to FP16 (11 bits; rounding them to BF16 would add
 // as much error again as the BF16 output has); to keep them in FP16's range
@@ -216,7 +217,7 @@ __device__ __forceinline__ void load_scales(const PagedAttnArgs& p, const Heads&
 // A tile's codes in registers.
 template <int D>
 struct Tile {
-  int k[2][D / 16];     // D / 4 bytes of a token in each half
+  int k[2][D / 16];     // D / 4 bytes of a token in each half, 16 of every 64
   int v[2][4][D / 64];  // D / 16 bytes of four tokens in each half
 };
 
@@ -241,7 +242,7 @@ __device__ __forceinline__ void load_k(const PagedAttnArgs& p, const Heads& hd, 
     const uint8_t* kp = hd.k + page_offset(page_of(p, pages, u, &ok), p.skc_p) + slot * p.skc_t;
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
-      const i32x4 v = load_codes<ONCE, i32x4>(kp + lane + 16 * j);
+      const i32x4 v = load_codes<ONCE, i32x4>(kp + lane + 64 * j);
 #pragma unroll
       for (int e = 0; e < 4; ++e) x.k[u][4 * j + e] = v[e];
     }
@@ -503,7 +504,7 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
   __shared__ int red[ATTN_WAVES], found[3];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int r16 = lane & 15, g4 = lane >> 4;
-  const uint32_t k_lane = (uint32_t)(r16 * p.skc_t + g4 * KB);
+  const uint32_t k_lane = (uint32_t)(r16 * p.skc_t + g4 * 16);
   const uint32_t v_lane = (uint32_t)(4 * g4 * p.svc_t + r16 * VB);
   const float qk = p.scale * LOG2E;
   const int streams = uniform(ATTN_WAVES / p.wr), stream = uniform(wave / p.wr), wgroup = wave - stream * p.wr;
@@ -541,7 +542,7 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
     const int lo_any = p.window > 0 && hi_all - p.window + 1 > 0 ? hi_all - p.window + 1 : 0;
     const int lo_all = p.window > 0 && hi_any - p.window + 1 > 0 ? hi_any - p.window + 1 : 0;
     Rows r[MT];
-    bf16x8 q[MT][D / 32];  // Q^T fragments: step j holds elements g4 * KB + 8 j ...
+    bf16x8 q[MT][D / 32];  // Q^T fragments: step j holds elements 64 (j / 2) + 16 g4 + 8 (j % 2) ...
     RowState<D> st[MT];
 #pragma unroll
     for (int k = 0; k < MT; ++k) {
@@ -551,11 +552,11 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
       const int qpos = len - p.n + qi;
       r[k].see_hi = row_ok ? qpos : -1;
       r[k].see_lo = p.window > 0 && qpos - p.window + 1 > 0 ? qpos - p.window + 1 : 0;
-      const uint16_t* from = p.q + s * p.sq_s + (int64_t)qi * p.sq_n + (int64_t)qh * p.sq_h + g4 * KB;
+      const uint16_t* from = p.q + s * p.sq_s + (int64_t)qi * p.sq_n + (int64_t)qh * p.sq_h + g4 * 16;
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
         i32x4 v = {0, 0, 0, 0};
-        if (row_ok) v = *reinterpret_cast<const i32x4*>(from + 8 * j);
+        if (row_ok) v = *reinterpret_cast<const i32x4*>(from + 64 * (j / 2) + 8 * (j % 2));
         q[k][j] = __builtin_bit_cast(bf16x8, v);
       }
 #pragma unroll
@@ -675,14 +676,14 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
 }
 
 // Join of the units that were cut: a workgroup takes `rps` rows (a power of
-// two) of a unit; its threads are D / 4 column quadruples x rps rows x GROUPS
-// that walk the parts in turn and are summed in order, so that the result does
-// not depend on anything but the lengths.
+// two) of a unit; its threads are D / 4 column quadruples x rps rows x groups
+// that walk the parts in turn, each with a running maximum, and are joined in
+// order, so that the result does not depend on anything but the lengths.
 template <int D>
 __global__ __launch_bounds__(ATTN_THREADS) void paged_attention_join_kernel(const PagedAttnArgs p) {
   constexpr int C = D / 4;
-  __shared__ f32x4 acc[ATTN_THREADS];
-  __shared__ float red[ATTN_WAVES][16];
+  __shared__ f32x4 so[ATTN_THREADS];
+  __shared__ float sm[ATTN_THREADS / C], sl[ATTN_THREADS / C];
   const int unit_rows = p.rt * 16, slices = unit_rows / p.rps;
   const int64_t u = blockIdx.x / slices;
   const int32_t* parts = unit_parts(p, u);
@@ -695,47 +696,37 @@ __global__ __launch_bounds__(ATTN_THREADS) void paged_attention_join_kernel(cons
   const int n = w1 - w0 + 1;
   const int64_t part_size = unit_rows * (D + 2);
   const float* base = part_at<D>(p, 2 * (int64_t)w0);  // part i at 2 i, the first one at 1
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-
-  // maxima of the rows: lane r of every rps lanes takes row r
-  const int rr = threadIdx.x % p.rps;
-  float m = -INFINITY;
-  for (int i = threadIdx.x / p.rps; i < n; i += ATTN_THREADS / p.rps)
-    m = fmaxf(m, base[(i == 0 ? 1 : 2 * (int64_t)i) * part_size + unit_rows * D + r0 + rr]);
-  for (int off = p.rps; off < 64; off <<= 1) m = fmaxf(m, __shfl_xor(m, off, 64));
-  if (lane < p.rps) red[wave][lane] = m;
-  __syncthreads();
 
   const int c = threadIdx.x % C, r = threadIdx.x / C % p.rps, g = threadIdx.x / C / p.rps;
-  const int n_groups = ATTN_THREADS / C / p.rps;
-  m = red[0][r];
-#pragma unroll
-  for (int w = 1; w < ATTN_WAVES; ++w) m = fmaxf(m, red[w][r]);
+  const int groups = ATTN_THREADS / C / p.rps;
   f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-  float l = 0.0f;
-#pragma unroll 4
-  for (int i = g; i < n; i += n_groups) {
-    const float* part = base + (i == 0 ? 1 : 2 * (int64_t)i) * part_size;
-    const float pm = part[unit_rows * D + r0 + r];
-    const float pl = part[unit_rows * (D + 1) + r0 + r];
-    const f32x4 v = *reinterpret_cast<const f32x4*>(part + (r0 + r) * D + 4 * c);
-    const float f = pm == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(pm - m);
-    l = __builtin_fmaf(pl, f, l);
+  float m = -INFINITY, l = 0.0f;
+  // (a part without a maximum has sums of 0, or of NaN where every score is NaN)
+  auto add = [&](f32x4 v, float pm, float pl) {
+    const float top = fmaxf(m, pm);
+    const float f = m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(m - top);
+    const float e = pm == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(pm - top);
+    m = top;
+    l = __builtin_fmaf(pl, e, l * f);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[e] = __builtin_fmaf(v[e], f, o[e]);
+    for (int i = 0; i < 4; ++i) o[i] = __builtin_fmaf(v[i], e, o[i] * f);
+  };
+#pragma unroll 4
+  for (int i = g; i < n; i += groups) {
+    const float* part = base + (i == 0 ? 1 : 2 * (int64_t)i) * part_size;
+    const float pm = part[unit_rows * D + r0 + r], pl = part[unit_rows * (D + 1) + r0 + r];
+    add(*reinterpret_cast<const f32x4*>(part + (r0 + r) * D + 4 * c), pm, pl);
   }
-  if (n_groups > 1) {
-    __syncthreads();  // the maxima have been read
-    acc[threadIdx.x] = o;
-    if (c == 0) (&red[0][0])[g * p.rps + r] = l;
+  if (groups > 1) {
+    so[threadIdx.x] = o;
+    if (c == 0) {
+      sm[g * p.rps + r] = m;
+      sl[g * p.rps + r] = l;
+    }
     __syncthreads();
     if (g > 0) return;
-    for (int k = 1; k < n_groups; ++k) {
-      const f32x4 v = acc[threadIdx.x + k * C * p.rps];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[e] += v[e];
-      l += (&red[0][0])[k * p.rps + r];
-    }
+    for (int k = 1; k < groups; ++k)
+      add(so[threadIdx.x + k * C * p.rps], sm[k * p.rps + r], sl[k * p.rps + r]);
   }
   if (row0 + r < p.rows) store_row<D>(p, s, h, row0 + r, 4 * c, o, m, l);
 }
@@ -826,13 +817,15 @@ hipError_t launch_paged_attention(PagedAttnArgs p, hipStream_t stream) {
   p.min_share = a.min_share;
   p.rps = a.rps;
   p.log_p = __builtin_ctz(p.P);
-  // Past the caches where no waves share codes and the sequences can hold more
-  // than the 256 MiB that the last-level cache keeps from call to call.  With /
-  // without, at D = 128: 128 sequences up to 8192 long (2 GiB at most) 198 / 211
-  // us, 4 up to 131071 long 71 / 81 us, 64 of 1024 to 2048 39.7 / 43.4 us, of
-  // 512 to 1024 (128 MiB) 22.7 / 20.8 us; with codes shared by two waves 44 / 33 us.
-  const bool once = a.rt == a.mt && p.groups == 1 &&
-                    2 * (int64_t)p.S * p.Hkv * p.max_pages * p.P * p.D >= (int64_t(256) << 20);
+  // Past the caches where no waves share codes and what the sequences can hold
+  // (of a window, what it can see) is more than the 256 MiB that the last-level
+  // cache keeps from call to call.  With / without, at D = 128: 128 sequences up
+  // to 8192 long (2 GiB at most) 198 / 218 us, 4 up to 131071 long 71 / 81 us, 64
+  // of 1024 to 2048 39.7 / 43.4 us, of 512 to 1024 (128 MiB) 22.7 / 20.8 us; with
+  // codes shared by two waves 44 / 33 us.
+  int64_t seen = (int64_t)p.max_pages * p.P;
+  if (p.window > 0 && seen > (int64_t)p.window + p.n) seen = (int64_t)p.window + p.n;
+  const bool once = a.rt == a.mt && p.groups == 1 && 2 * (int64_t)p.S * p.Hkv * seen * p.D >= (int64_t(256) << 20);
 #define ATTN_CASE(D_, MT)                              \
   if (p.D == D_ && a.mt == MT)                         \
     return once ? launch<D_, MT, true>(p, a, stream) : launch<D_, MT, false>(p, a, stream);
