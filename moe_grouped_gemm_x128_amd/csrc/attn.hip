@@ -539,8 +539,8 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
     const int qi_first = uniform(wrow0 / p.group);
     const int qi_last = uniform((wrow0 + 16 * MT < p.rows ? wrow0 + 16 * MT - 1 : p.rows - 1) / p.group);
     const int hi_all = len - p.n + qi_first, hi_any = len - p.n + qi_last;
-    const int lo_any = p.window > 0 && hi_all - p.window + 1 > 0 ? hi_all - p.window + 1 : 0;
-    const int lo_all = p.window > 0 && hi_any - p.window + 1 > 0 ? hi_any - p.window + 1 : 0;
+    const int lo_any = p.window > 0 && hi_all >= p.window ? hi_all - p.window + 1 : 0;
+    const int lo_all = p.window > 0 && hi_any >= p.window ? hi_any - p.window + 1 : 0;
     Rows r[MT];
     bf16x8 q[MT][D / 32];  // Q^T fragments: step j holds elements 64 (j / 2) + 16 g4 + 8 (j % 2) ...
     RowState<D> st[MT];
@@ -551,7 +551,7 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
       const int qi = row_ok ? row / p.group : 0, qh = h * p.group + (row_ok ? row - qi * p.group : 0);
       const int qpos = len - p.n + qi;
       r[k].see_hi = row_ok ? qpos : -1;
-      r[k].see_lo = p.window > 0 && qpos - p.window + 1 > 0 ? qpos - p.window + 1 : 0;
+      r[k].see_lo = p.window > 0 && qpos >= p.window ? qpos - p.window + 1 : 0;
       const uint16_t* from = p.q + s * p.sq_s + (int64_t)qi * p.sq_n + (int64_t)qh * p.sq_h + g4 * 16;
 #pragma unroll
       for (int j = 0; j < D / 32; ++j) {
@@ -752,12 +752,12 @@ AttnPlan attn_plan(int64_t S, int64_t Hkv, int64_t row_tiles, int64_t D, int64_t
   a.units = (int)(Hkv * ((row_tiles + a.rt - 1) / a.rt));
   const int64_t cap_tiles = (cap + 31) / 32, units = S * a.units;
   // Short caches are not cut, the longer the more units there are to fill the
-  // machine: the cut costs the scans of the lengths and the join's launch, about
-  // 7 us.  Not cut / cut, in us (cache capacity; lengths from half of it up):
-  // 8 units of D = 128: 1024 tokens 10.5 / 11.5, 2048 tokens 16.4 / 11.8;
-  // 128 units: 2048 tokens 19.7 / 22.8, 4096 tokens 35.0 / 30.3;
-  // 512 units: 2048 tokens 42.8 / 54.0, 4096 tokens 78.5 / 90.3;
-  // 1024 units of lengths from 1 to 8192: 279 / 217.
+  // machine: the cut costs the scans of the lengths and the join's launch, 3 to
+  // 10 us.  Not cut / cut, in us (cache capacity; lengths from half of it up;
+  // D = 128): 8 units: 1024 tokens 10.5 / 10.4, 2048 tokens 16.6 / 10.9;
+  // 128 units: 2048 tokens 19.8 / 22.7, 4096 tokens 33.9 / 29.8;
+  // 512 units: 2048 tokens 41 / 48, 4096 tokens 76 / 82, 8192 tokens 151 / 144;
+  // 1024 units of lengths from 1 to 8192: 279 / 204.
   const int64_t direct = 32 + units / 4;
   a.split = cap_tiles > (direct < 128 ? direct : 128);
   a.min_share = ATTN_WAVES / a.wr;  // a tile for each stream
@@ -808,7 +808,12 @@ int64_t paged_attention_grid(int64_t S, int64_t Hkv, int64_t row_tiles, int64_t 
 }
 
 hipError_t launch_paged_attention(PagedAttnArgs p, hipStream_t stream) {
-  const AttnPlan a = attn_plan(p.S, p.Hkv, p.row_tiles, p.D, (int64_t)p.max_pages * p.P);
+  // what a sequence can hold or, of a window, its queries can see (its first
+  // tile may begin up to 31 positions before that); the plan for it needs no
+  // more workspace than the whole capacity's
+  int64_t seen = (int64_t)p.max_pages * p.P;
+  if (p.window > 0 && seen > (int64_t)p.window + p.n + 31) seen = (int64_t)p.window + p.n + 31;
+  const AttnPlan a = attn_plan(p.S, p.Hkv, p.row_tiles, p.D, seen);
   p.rt = a.rt;
   p.wr = a.wr;
   p.units = a.units;
@@ -818,13 +823,11 @@ hipError_t launch_paged_attention(PagedAttnArgs p, hipStream_t stream) {
   p.rps = a.rps;
   p.log_p = __builtin_ctz(p.P);
   // Past the caches where no waves share codes and what the sequences can hold
-  // (of a window, what it can see) is more than the 256 MiB that the last-level
-  // cache keeps from call to call.  With / without, at D = 128: 128 sequences up
+  // or see is more than the 256 MiB that the last-level cache keeps from call
+  // to call.  With / without, at D = 128: 128 sequences up
   // to 8192 long (2 GiB at most) 198 / 218 us, 4 up to 131071 long 71 / 81 us, 64
   // of 1024 to 2048 39.7 / 43.4 us, of 512 to 1024 (128 MiB) 22.7 / 20.8 us; with
   // codes shared by two waves 44 / 33 us.
-  int64_t seen = (int64_t)p.max_pages * p.P;
-  if (p.window > 0 && seen > (int64_t)p.window + p.n) seen = (int64_t)p.window + p.n;
   const bool once = a.rt == a.mt && p.groups == 1 && 2 * (int64_t)p.S * p.Hkv * seen * p.D >= (int64_t(256) << 20);
 #define ATTN_CASE(D_, MT)                              \
   if (p.D == D_ && a.mt == MT)                         \

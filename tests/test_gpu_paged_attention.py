@@ -154,6 +154,20 @@ def test_long_caches_with_many_rows(D, P, S, n, H, group, window, lens):
     _compare(c, out, lse, D ** -0.5, window, "long, many rows")
 
 
+@pytest.mark.parametrize("D,P,S,n,H,group,window,lens", [
+    (128, 64, 3, 1, 2, 4, 300, [9000, 8192, 299]),   # what a query sees fits the uncut form, the table does not
+    (64, 16, 2, 4, 1, 8, 1500, [6001, 40]),          # cut
+    (256, 32, 2, 2, 1, 4, 31, [4100, 4097]),         # the window's positions in two tiles
+    (128, 16, 1, 1, 1, 8, 1 << 30, [4500]),          # a window longer than any cache
+    (128, 64, 2, 9, 1, 4, 2**31 - 1, [4400, 2]),     # the largest window, queries from before the first position
+])
+def test_windows_in_long_caches(D, P, S, n, H, group, window, lens):
+    say(f"paged_attention_fp8 windows D={D} P={P} n={n} group={group} window={window} lens={lens}")
+    c = _case(D + n + group, S, n, H * group, H, D, P, lens)
+    out, lse = _run(c, D ** -0.5, window)
+    _compare(c, out, lse, D ** -0.5, window, "window")
+
+
 def test_more_sequences_than_threads():
     """Six hundred sequences, most of them short or empty, in a table wide
     enough for the work to be cut along the cache; and without a cut."""
