@@ -72,6 +72,14 @@ __device__ __forceinline__ int uniform_load(const int32_t* p) { return *(const_i
 __device__ __forceinline__ float uniform_load(const float* p) { return *(const_f32)(uintptr_t)p; }
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
+// A barrier for what passes through shared memory alone: loads and stores of
+// global memory go on meanwhile.
+__device__ __forceinline__ void local_barrier() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // Tiles of 32 positions that the queries of sequence s look at: [begin, end).
 // A sequence whose queries see nothing has one tile (of masked positions), so
 // that every unit is somebody's work.
@@ -120,40 +128,74 @@ __device__ __forceinline__ int line_scan(int v, int* red, int* all) {
   return v;
 }
 
-// Tiles of sequence s on the line of all units' tiles (the line is below 2^31).
-__device__ __forceinline__ int line_tiles(const PagedAttnArgs& p, int s, int* len) {
+__device__ __forceinline__ int padded(int tiles, int pad) { return (tiles + pad - 1) / pad * pad; }
+
+// Places of sequence s on the line of all units' tiles (the line is below
+// 2^31): a unit's tiles, rounded up to a multiple of pad.
+__device__ __forceinline__ int line_tiles(const PagedAttnArgs& p, int s, int pad, int* len) {
   *len = s < p.S ? p.lens[s] : 0;
   const Span sp = span_of(p, *len);
-  return s < p.S ? (sp.end - sp.begin) * p.units : 0;
+  return s < p.S ? padded(sp.end - sp.begin, pad) * p.units : 0;
 }
 
 // This workgroup's part [at, end) of the line, the sequence in which it begins
-// and the tiles before that one.
+// and the places before that one; pad as above.
 struct Share {
-  int size, at, end, before, s, len;
+  int size, pad, at, end, before, s, len;
 };
 
-// false: nothing for this workgroup.
-__device__ __forceinline__ bool line_share(const PagedAttnArgs& p, int* red, int* found, Share& o) {
-  int len, total;
-  int mine = line_tiles(p, threadIdx.x, &len);
-  int upto = line_scan(mine, red, &total);
-  for (int base = ATTN_THREADS; base < p.S; base += ATTN_THREADS) {  // (more sequences than threads)
-    int l, all;
-    line_scan(line_tiles(p, base + threadIdx.x, &l), red, &all);
-    total += all;
-  }
-  const int n = (int)(((uint32_t)total + p.shares - 1) / p.shares);
-  o.size = n < p.min_share ? p.min_share : n;
+// A share's size: an equal part of all tiles, in whole places.
+__device__ __forceinline__ void share_size(const PagedAttnArgs& p, int total, Share& o) {
+  const int n = (int)(((uint32_t)total + p.cuts - 1) / p.cuts);
+  o.size = uniform(n < p.min_share ? p.min_share : n);
+  o.pad = p.whole ? o.size : 1;  // (whole: no share reaches past its unit)
+}
+// false: it begins past the line's end.
+__device__ __forceinline__ bool share_place(int total, Share& o) {
   const int64_t at = (int64_t)blockIdx.x * o.size;
   if (at >= total) return false;
   o.at = (int)at;
   o.end = at + o.size < total ? o.at + o.size : total;
+  return true;
+}
+
+// false: nothing for this workgroup.
+__device__ __forceinline__ bool line_share(const PagedAttnArgs& p, int* red, int* found, Share& o) {
+  int len, total;
+  if (p.S <= 64) {  // a lane a sequence, every wave by itself
+    const int lane = threadIdx.x & 63;
+    int mine = line_tiles(p, lane, 1, &len);
+    int upto = wave_scan(mine);
+    share_size(p, __builtin_amdgcn_readlane(upto, 63), o);
+    if (o.pad > 1) {
+      mine = line_tiles(p, lane, o.pad, &len);
+      upto = wave_scan(mine);
+    }
+    if (!share_place(__builtin_amdgcn_readlane(upto, 63), o)) return false;
+    o.s = __builtin_ctzll(__ballot(o.at < upto));  // the first one that ends past it
+    o.before = __builtin_amdgcn_readlane(upto - mine, o.s);
+    o.len = __builtin_amdgcn_readlane(len, o.s);
+    return true;
+  }
+  int mine, upto;
+  const auto scan_all = [&](int pad) {  // (mine, upto: of the first ATTN_THREADS sequences)
+    mine = line_tiles(p, threadIdx.x, pad, &len);
+    upto = line_scan(mine, red, &total);
+    for (int base = ATTN_THREADS; base < p.S; base += ATTN_THREADS) {
+      int l, all;
+      line_scan(line_tiles(p, base + threadIdx.x, pad, &l), red, &all);
+      total += all;
+    }
+  };
+  scan_all(1);
+  share_size(p, total, o);
+  if (o.pad > 1) scan_all(o.pad);
+  if (!share_place(total, o)) return false;
   int before = 0;
   for (int base = 0;; base += ATTN_THREADS) {
     if (p.S > ATTN_THREADS) {
       int all;
-      mine = line_tiles(p, base + threadIdx.x, &len);
+      mine = line_tiles(p, base + threadIdx.x, o.pad, &len);
       upto = before + line_scan(mine, red, &all);
       before += all;
     }
@@ -498,9 +540,9 @@ template <int D, int MT, bool SPLIT, bool ONCE>
 __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_attention_kernel(const PagedAttnArgs p) {
   constexpr int KB = D / 4;    // bytes of a key per lane
   constexpr int VB = D / 16;   // bytes of a value per lane, and output tiles
-  constexpr int CW = D < 128 ? D : 128;  // columns that the waves join at a time
-  __shared__ float so[ATTN_WAVES][16][CW + 4];
+  __shared__ float so[ATTN_WAVES][16][D + 4];  // a row tile's sums of every wave
   __shared__ float sm[MT][ATTN_WAVES][16], sl[MT][ATTN_WAVES][16];
+  __shared__ float row_m[ATTN_WAVES][16], row_l[ATTN_WAVES][16];
   __shared__ int red[ATTN_WAVES], found[3];
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int r16 = lane & 15, g4 = lane >> 4;
@@ -509,7 +551,7 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
   const float qk = p.scale * LOG2E;
   const int streams = uniform(ATTN_WAVES / p.wr), stream = uniform(wave / p.wr), wgroup = wave - stream * p.wr;
 
-  Share line = {0, 0, 1, 0, 0, 0};
+  Share line = {0, 1, 0, 1, 0, 0, 0};
   if (SPLIT) {
     if (!line_share(p, red, found, line)) return;
   } else {
@@ -521,15 +563,16 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
     const int s = line.s;
     const Span sp = span_of(p, line.len);
     const int nt = sp.end - sp.begin;
-    if (SPLIT && line.at - line.before >= nt * p.units) {  // next sequence
-      line.before += nt * p.units;
+    const int places = SPLIT ? padded(nt, line.pad) : nt;
+    if (SPLIT && line.at - line.before >= places * p.units) {  // next sequence
+      line.before += places * p.units;
       ++line.s;
       line.len = uniform_load(p.lens + line.s);
       continue;
     }
     const int rel = line.at - line.before;
-    const int unit = uniform(SPLIT ? rel / nt : (int)(blockIdx.x - s * p.units));
-    const int t0 = SPLIT ? rel - unit * nt : 0;
+    const int unit = uniform(SPLIT ? rel / places : (int)(blockIdx.x - s * p.units));
+    const int t0 = SPLIT ? rel - unit * places : 0;
     const int t1 = SPLIT && line.end - line.at < nt - t0 ? t0 + line.end - line.at : nt;
     const int h = uniform(unit / p.groups), row0 = (unit - h * p.groups) * p.wr * MT * 16;
     const int len = sp.len;
@@ -610,7 +653,7 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
 
     // join the waves: each scales its output to the common maximum, then every
     // thread sums four columns of a row
-    if (SPLIT) __syncthreads();  // the last piece's join has been read
+    if (SPLIT) local_barrier();  // the last piece's join has been read
 #pragma unroll
     for (int k = 0; k < MT; ++k) {
       st[k].l = quarters(st[k].l, [](float a, float b) { return a + b; });
@@ -619,48 +662,59 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
         sl[k][wave][r16] = st[k].l;
       }
     }
+    local_barrier();
     const bool piece = t0 > 0 || t1 < nt;
     float* part = piece ? part_at<D>(p, 2 * (int64_t)blockIdx.x + (t0 == 0)) : nullptr;
 #pragma unroll
     for (int k = 0; k < MT; ++k) {
       if (row0 + 16 * k >= p.rows) break;
+      float m = -INFINITY, l = 0.0f;
+      for (int w = wgroup; w < ATTN_WAVES; w += p.wr) m = fmaxf(m, sm[k][w][r16]);
+      // (without a maximum the sums are 0, or NaN where every score is NaN)
+      for (int w = wgroup; w < ATTN_WAVES; w += p.wr)
+        l += sl[k][w][r16] * (sm[k][w][r16] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(sm[k][w][r16] - m));
+      const float f = st[k].m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st[k].m - m);
+      if (k > 0) local_barrier();  // the last row tile's sums have been read
+      // element (i, e) of the lane is output element g4 * KB + e * VB + i
 #pragma unroll
-      for (int c0 = 0; c0 < D; c0 += CW) {
-        __syncthreads();
-        // element (i, e) of the lane is output element g4 * KB + e * VB + i
-        if (g4 * KB >= c0 && g4 * KB < c0 + CW) {
-          float m = -INFINITY;
-          for (int w = wgroup; w < ATTN_WAVES; w += p.wr) m = fmaxf(m, sm[k][w][r16]);
-          // (without a maximum the sums are 0, or NaN where every score is NaN)
-          const float f = st[k].m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st[k].m - m);
+      for (int e = 0; e < 4; ++e)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
+        for (int i = 0; i < VB; i += 4)
+          *reinterpret_cast<f32x4*>(&so[wave][r16][g4 * KB + e * VB + i]) =
+              f32x4{st[k].o[i][e] * f, st[k].o[i + 1][e] * f, st[k].o[i + 2][e] * f, st[k].o[i + 3][e] * f};
+      if (stream == 0 && g4 == 0) {
+        row_m[wgroup][r16] = m;
+        row_l[wgroup][r16] = l;
+      }
+      local_barrier();
+      constexpr int TAKE = D / 64;  // of the row tile's D / 4 x 16 quadruples
+      f32x4 sum[TAKE];
+      for (int g = 0; g < p.wr; ++g) {
 #pragma unroll
-            for (int i = 0; i < VB; i += 4)
-              *reinterpret_cast<f32x4*>(&so[wave][r16][g4 * KB - c0 + e * VB + i]) =
-                  f32x4{st[k].o[i][e] * f, st[k].o[i + 1][e] * f, st[k].o[i + 2][e] * f, st[k].o[i + 3][e] * f};
+        for (int i = 0; i < TAKE; ++i) {
+          const int j = threadIdx.x + i * ATTN_THREADS, c = j % (D / 4) * 4, rw = j / (D / 4);
+          sum[i] = *reinterpret_cast<const f32x4*>(&so[g][rw][c]);
         }
-        __syncthreads();
-        for (int j = threadIdx.x; j < p.wr * 16 * (CW / 4); j += ATTN_THREADS) {
-          const int c = j % (CW / 4) * 4, rw = j / (CW / 4) % 16, g = j / (CW / 4) / 16, rr = (g * MT + k) * 16 + rw;
-          if (row0 + rr >= p.rows) continue;
-          f32x4 o = {0.0f, 0.0f, 0.0f, 0.0f};
-          float mm = -INFINITY, ll = 0.0f;
-          for (int w = g; w < ATTN_WAVES; w += p.wr) mm = fmaxf(mm, sm[k][w][rw]);
-          for (int w = g; w < ATTN_WAVES; w += p.wr) {
+        for (int w = g + p.wr; w < ATTN_WAVES; w += p.wr)
+#pragma unroll
+          for (int i = 0; i < TAKE; ++i) {
+            const int j = threadIdx.x + i * ATTN_THREADS, c = j % (D / 4) * 4, rw = j / (D / 4);
             const f32x4 v = *reinterpret_cast<const f32x4*>(&so[w][rw][c]);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[e] += v[e];
-            ll += sl[k][w][rw] * (sm[k][w][rw] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(sm[k][w][rw] - mm));
+            for (int e = 0; e < 4; ++e) sum[i][e] += v[e];
           }
+#pragma unroll
+        for (int i = 0; i < TAKE; ++i) {
+          const int j = threadIdx.x + i * ATTN_THREADS, c = j % (D / 4) * 4, rw = j / (D / 4), rr = (g * MT + k) * 16 + rw;
+          if (row0 + rr >= p.rows) continue;
           if (SPLIT && piece) {
-            *reinterpret_cast<f32x4*>(part + rr * D + c0 + c) = o;
-            if (c0 + c == 0) {
-              part[p.rt * 16 * D + rr] = mm;
-              part[p.rt * 16 * (D + 1) + rr] = ll;
+            *reinterpret_cast<f32x4*>(part + rr * D + c) = sum[i];
+            if (c == 0) {
+              part[p.rt * 16 * D + rr] = row_m[g][rw];
+              part[p.rt * 16 * (D + 1) + rr] = row_l[g][rw];
             }
           } else {
-            store_row<D>(p, s, h, row0 + rr, c0 + c, o, mm, ll);
+            store_row<D>(p, s, h, row0 + rr, c, sum[i], row_m[g][rw], row_l[g][rw]);
           }
         }
       }
@@ -671,6 +725,7 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
       parts[0] = blockIdx.x;
       parts[1] = (line.at + nt - 1) / line.size;
     }
+    if (line.pad > 1) return;
     line.at += t1 - t0;
   }
 }
@@ -737,6 +792,7 @@ struct AttnPlan {
   int units;            // units (KV head, group of row tiles) per sequence
   bool split;
   int64_t shares;       // workgroups of the first kernel when split
+  bool whole;           // a share is of one unit
   int min_share;        // tiles of a share at least
   int rps;              // rows per workgroup of the join
 };
@@ -771,6 +827,11 @@ AttnPlan attn_plan(int64_t S, int64_t Hkv, int64_t row_tiles, int64_t D, int64_t
   if (most > fit) most = fit;
   const int64_t want = (units * cap_tiles + a.min_share - 1) / a.min_share;
   a.shares = want < most ? want : most;
+  // Few units have each its own count of shares, the last one what is left: the
+  // tiles are divided by (shares - units), and the roundings up need no more
+  // than the rest.  Else shares that begin in one unit and end in another take
+  // half as long again as the others, most of it waiting for a second first tile.
+  a.whole = 4 * units <= a.shares && units * cap_tiles < (int64_t(1) << 30);
   // few units: a row to a workgroup; many: as many rows as its threads hold
   a.rps = (int)(ATTN_THREADS / (D / 4));
   if (a.rps > 16) a.rps = 16;
@@ -820,6 +881,8 @@ hipError_t launch_paged_attention(PagedAttnArgs p, hipStream_t stream) {
   p.groups = a.units / p.Hkv;
   p.shares = (int32_t)a.shares;
   p.min_share = a.min_share;
+  p.whole = a.whole;
+  p.cuts = (int32_t)(a.whole ? a.shares - (int64_t)p.S * a.units : a.shares);
   p.rps = a.rps;
   p.log_p = __builtin_ctz(p.P);
   // Past the caches where no waves share codes and what the sequences can hold

@@ -165,11 +165,13 @@ struct PagedAttnArgs {
   int32_t S, n, Hkv, group, rows, row_tiles, D, P, max_pages, pages, window;
   float scale;
   float* workspace;
-  // set by the launcher: row tiles of a unit, waves that take
-  // them side by side, units (KV head,
-  // group of row tiles) per sequence, groups per head, workgroups of the first kernel, tiles a
-  // workgroup takes at least, rows per workgroup of the join, log2 P
-  int32_t rt, wr, units, groups, shares, min_share, rps, log_p;
+  // set by the launcher: row tiles of a unit, waves that take them side by
+  // side, units (KV head, group of row tiles) per sequence, groups per head,
+  // workgroups of the first kernel, what all tiles are divided by for a share's
+  // size, tiles a workgroup takes at least, rows per workgroup of the join,
+  // log2 P; a share is of one unit
+  int32_t rt, wr, units, groups, shares, cuts, min_share, rps, log_p;
+  bool whole;
 };
 
 struct PackArgs {

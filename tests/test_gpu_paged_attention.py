@@ -168,6 +168,18 @@ def test_windows_in_long_caches(D, P, S, n, H, group, window, lens):
     _compare(c, out, lse, D ** -0.5, window, "window")
 
 
+def test_shares_of_whole_units():
+    """Eighty sequences (more than a wave has lanes), few enough that every
+    share is of one unit; some end in a short last share, some are empty."""
+    say("paged_attention_fp8 80 sequences cut into whole shares")
+    rng = np.random.default_rng(80)
+    lens = [int(x) for x in rng.integers(0, 1800, 80)]
+    lens[0], lens[1], lens[40], lens[79] = 0, 1, 2304, 2304
+    c = _case(80, 80, 2, 4, 1, 64, 64, lens)
+    out, lse = _run(c, 0.125)
+    _compare(c, out, lse, 0.125, 0, "whole shares")
+
+
 def test_more_sequences_than_threads():
     """Six hundred sequences, most of them short or empty, in a table wide
     enough for the work to be cut along the cache; and without a cut."""
