@@ -51,11 +51,13 @@ typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
 
+constexpr int CUS = 256;
 constexpr int ATTN_WAVES = 4;
 constexpr int ATTN_THREADS = 64 * ATTN_WAVES;
 // Waves per SIMD that the registers are held to: the output takes D / 4 MT
 // registers of a lane, the queries D / 8 MT, a tile's codes D / 4.
 constexpr int WAVES_PER_SIMD(int D, int MT) { return D * MT <= 128 ? 3 : 2; }
+constexpr int FEW_TILES = 32;
 constexpr float P_GAIN = 16384.0f;  // weights are held times 2^14 in FP16
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
 
@@ -144,10 +146,16 @@ struct Share {
   int size, pad, at, end, before, s, len;
 };
 
-// A share's size: an equal part of all tiles, in whole places.
+// A share's size: an equal part of all tiles for two workgroups of every
+// compute unit, or for one where that is at most FEW_TILES, as a share costs its
+// start and the join of its part whatever its size.  Two / one, in us: 8 units
+// of up to 256 tiles, D = 256 and 32 rows 21.8 / 19.5; 6 units of up to 940
+// tiles, D = 256 25.4 / 22.8; 8 units of 256 tiles, D = 128 13.1 / 14.3.
 __device__ __forceinline__ void share_size(const PagedAttnArgs& p, int total, Share& o) {
-  const int n = (int)(((uint32_t)total + p.cuts - 1) / p.cuts);
-  o.size = uniform(n < p.min_share ? p.min_share : n);
+  const int one = (int)(((uint32_t)total + p.cuts_one - 1) / p.cuts_one);
+  int n = (int)(((uint32_t)total + p.cuts - 1) / p.cuts);
+  if (one <= FEW_TILES) n = one;
+  o.size = uniform((n + p.min_share - 1) & -p.min_share);  // as many tiles for each stream of waves
   o.pad = p.whole ? o.size : 1;  // (whole: no share reaches past its unit)
 }
 // false: it begins past the line's end.
@@ -793,7 +801,7 @@ struct AttnPlan {
   bool split;
   int64_t shares;       // workgroups of the first kernel when split
   bool whole;           // a share is of one unit
-  int min_share;        // tiles of a share at least
+  int min_share;        // tiles of a share: a multiple of this power of two
   int rps;              // rows per workgroup of the join
 };
 
@@ -817,11 +825,12 @@ AttnPlan attn_plan(int64_t S, int64_t Hkv, int64_t row_tiles, int64_t D, int64_t
   const int64_t direct = 32 + units / 4;
   a.split = cap_tiles > (direct < 128 ? direct : 128);
   a.min_share = ATTN_WAVES / a.wr;  // a tile for each stream
-  // Shares: as many workgroups as are resident at once on 256 compute units,
-  // so that all end together.  At D = 128 512 / 768 / 1024 shares took 223 /
-  // 219 / 227 us (128 sequences up to 8192 long, 8 heads) and 80 / 82 / 85 us
-  // (4 sequences up to 131071 long, 4 heads).
-  int64_t most = 256 * WAVES_PER_SIMD((int)D, a.mt);
+  // Shares: two workgroups a compute unit, resident at once, so that all end
+  // together (its registers would hold a third at D <= 128).  256 / 512 / 768 /
+  // 1024 shares, in us, at D = 128: 128 sequences up to 8192 long, 8 heads 226 /
+  // 207 / 211 / 225; 4 sequences up to 131071 long, 4 heads 83 / 79 / 80 / 87;
+  // few tiles (2 sequences up to 16384 long, 4 heads, 64 rows) 24 / 25.5 / 25.4 / 32.
+  int64_t most = 2 * CUS;
   // (and the parts of one call within 40 MiB)
   const int64_t fit = (int64_t(10) << 20) / (2 * a.rt * 16 * (D + 2));
   if (most > fit) most = fit;
@@ -882,7 +891,9 @@ hipError_t launch_paged_attention(PagedAttnArgs p, hipStream_t stream) {
   p.shares = (int32_t)a.shares;
   p.min_share = a.min_share;
   p.whole = a.whole;
-  p.cuts = (int32_t)(a.whole ? a.shares - (int64_t)p.S * a.units : a.shares);
+  const int64_t ends = a.whole ? (int64_t)p.S * a.units : 0;
+  p.cuts = (int32_t)(a.shares - ends);
+  p.cuts_one = (int32_t)((a.shares < CUS ? a.shares : CUS) - ends);
   p.rps = a.rps;
   p.log_p = __builtin_ctz(p.P);
   // Past the caches where no waves share codes and what the sequences can hold

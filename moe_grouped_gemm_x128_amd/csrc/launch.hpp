@@ -168,9 +168,9 @@ struct PagedAttnArgs {
   // set by the launcher: row tiles of a unit, waves that take them side by
   // side, units (KV head, group of row tiles) per sequence, groups per head,
   // workgroups of the first kernel, what all tiles are divided by for a share's
-  // size, tiles a workgroup takes at least, rows per workgroup of the join,
-  // log2 P; a share is of one unit
-  int32_t rt, wr, units, groups, shares, cuts, min_share, rps, log_p;
+  // size (with two workgroups a compute unit, and with one), what the size is a
+  // multiple of, rows per workgroup of the join, log2 P; a share is of one unit
+  int32_t rt, wr, units, groups, shares, cuts, cuts_one, min_share, rps, log_p;
   bool whole;
 };
 
