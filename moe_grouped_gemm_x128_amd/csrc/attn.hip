@@ -552,6 +552,9 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
   __shared__ float sm[MT][ATTN_WAVES][16], sl[MT][ATTN_WAVES][16];
   __shared__ float row_m[ATTN_WAVES][16], row_l[ATTN_WAVES][16];
   __shared__ int red[ATTN_WAVES], found[3];
+  // (one argument of every 64-byte line, so that the lines come in together:
+  // 0.3 to 0.5 us of a short call)
+  asm volatile("" ::"s"(p.q), "s"(p.out), "s"(p.sl_s), "s"(p.skc_p), "s"(p.v_scale), "s"(p.lens), "s"(p.workspace), "s"(p.log_p));
   const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
   const int r16 = lane & 15, g4 = lane >> 4;
   const uint32_t k_lane = (uint32_t)(r16 * p.skc_t + g4 * 16);
