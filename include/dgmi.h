@@ -10,6 +10,8 @@
  *   "DeepInside DeepGEMM: Unpacking DeepSeek's Unified Tensor Core Library
  *    for SM90 and SM100", section 2 (NT layout, FP32 or packed UE8M0 scale
  *    factors) and section 4 (fp8_gemm_nt(a, b, a_sf, b_sf, c, bf16)).
+ * Around them: casts, the MoE steps (choice of experts, dispatch, combine),
+ * and a paged FP8 key/value cache with the attention over it.
  *
  * Conventions shared by every entry point
  *   - Every buffer is device memory allocated and owned by the caller,
@@ -51,7 +53,8 @@ enum {
 enum {
   DG_OK = 0,
   DG_INVALID_ARG = 1,   /* null / dtype / ndim / shape / stride / alignment / aliasing */
-  DG_UNSUPPORTED = 2,   /* legal but not implemented (K % 128 != 0; GEMM operand row strides of 8 MiB or more) */
+  DG_UNSUPPORTED = 2,   /* legal but not implemented (K % 128 != 0; GEMM operand row strides of 8 MiB or more;
+                         * more experts, head sizes or lengths than a kernel takes: see each call) */
   DG_LAUNCH_FAILED = 3  /* the HIP runtime rejected a launch */
 };
 
