@@ -241,35 +241,52 @@ struct Heads {
 };
 
 // The pages of a tile's two 16-token halves as the table has them, -1 past
-// the end.  One load where a page holds 32 tokens or more (the second is then
-// the first).
+// the end.  P16: a page holds 16 tokens; else the second half's is the first's.
 struct Pages {
   int id0, id1;
 };
+template <bool P16>
 __device__ __forceinline__ void find_pages(const PagedAttnArgs& p, const Heads& hd, int t, bool wanted, Pages& x) {
   x.id0 = x.id1 = -1;
   if (wanted && t * 32 < hd.len) x.id0 = uniform_load(hd.table + ((t * 32) >> p.log_p));
-  if (p.P == 16 && wanted && t * 32 + 16 < hd.len) x.id1 = uniform_load(hd.table + 2 * t + 1);
+  if (P16 && wanted && t * 32 + 16 < hd.len) x.id1 = uniform_load(hd.table + 2 * t + 1);
 }
 
 // Half u's page; page 0 is read where it takes no part (ok: it does).
+template <bool P16>
 __device__ __forceinline__ int page_of(const PagedAttnArgs& p, const Pages& x, int u, bool* ok) {
-  const int id = u == 0 || p.P > 16 ? x.id0 : x.id1;
+  const int id = P16 && u == 1 ? x.id1 : x.id0;
   *ok = id >= 0 && id < p.pages;
   return *ok ? id : 0;
 }
 // One page's place: strides are below 2^32 bytes, a page's tokens within 2^31.
 __device__ __forceinline__ uint64_t page_offset(int page, uint32_t stride) { return (uint64_t)(uint32_t)page * stride; }
 
+// Where half u's codes begin.
+template <bool P16>
+__device__ __forceinline__ const uint8_t* half_at(const PagedAttnArgs& p, const uint8_t* base, uint32_t page_step, uint32_t step,
+                                                  int t, const Pages& x, int u) {
+  bool ok;
+  const uint32_t slot = P16 ? 0 : ((t * 32) & (p.P - 1)) + 16 * u;
+  return base + page_offset(page_of<P16>(p, x, u, &ok), page_step) + slot * step;
+}
+
 // The scales of a tile's halves as they are stored.
 struct Scales {
   int ks[2], vs[2];
   bool ok[2];
 };
+template <bool P16>
 __device__ __forceinline__ void load_scales(const PagedAttnArgs& p, const Heads& hd, const Pages& pages, Scales& x) {
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const int page = page_of(p, pages, u, &x.ok[u]);
+    if (!P16 && u == 1) {
+      x.ks[1] = x.ks[0];
+      x.vs[1] = x.vs[0];
+      x.ok[1] = x.ok[0];
+      break;
+    }
+    const int page = page_of<P16>(p, pages, u, &x.ok[u]);
     x.ks[u] = uniform_load(reinterpret_cast<const int32_t*>(reinterpret_cast<const uint8_t*>(hd.ks) + page_offset(page, p.sks_p)));
     x.vs[u] = uniform_load(reinterpret_cast<const int32_t*>(reinterpret_cast<const uint8_t*>(hd.vs) + page_offset(page, p.svs_p)));
   }
@@ -292,15 +309,13 @@ __device__ __forceinline__ T load_codes(const uint8_t* at) {
 
 // lane: this lane's offset inside a 16-token half.  (Kept opaque, so that the
 // loads take a scalar base and a 32-bit offset.)
-template <int D, bool ONCE>
+template <int D, bool ONCE, bool P16>
 __device__ __forceinline__ void load_k(const PagedAttnArgs& p, const Heads& hd, int t, const Pages& pages, uint32_t lane,
                                        Tile<D>& x) {
   asm volatile("" : "+v"(lane));
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const int slot = (t * 32 + 16 * u) & (p.P - 1);
-    bool ok;
-    const uint8_t* kp = hd.k + page_offset(page_of(p, pages, u, &ok), p.skc_p) + slot * p.skc_t;
+    const uint8_t* kp = half_at<P16>(p, hd.k, p.skc_p, p.skc_t, t, pages, u);
 #pragma unroll
     for (int j = 0; j < D / 64; ++j) {
       const i32x4 v = load_codes<ONCE, i32x4>(kp + lane + 64 * j);
@@ -310,7 +325,7 @@ __device__ __forceinline__ void load_k(const PagedAttnArgs& p, const Heads& hd, 
   }
 }
 
-template <int D, bool ONCE>
+template <int D, bool ONCE, bool P16>
 __device__ __forceinline__ void load_v(const PagedAttnArgs& p, const Heads& hd, int t, const Pages& pages, uint32_t lane,
                                        Tile<D>& x) {
   constexpr int VB = D / 16;
@@ -322,9 +337,7 @@ __device__ __forceinline__ void load_v(const PagedAttnArgs& p, const Heads& hd, 
   }
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
-    const int slot = (t * 32 + 16 * u) & (p.P - 1);
-    bool ok;
-    const uint8_t* vp = hd.v + page_offset(page_of(p, pages, u, &ok), p.svc_p) + slot * p.svc_t;
+    const uint8_t* vp = half_at<P16>(p, hd.v, p.svc_p, p.svc_t, t, pages, u);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const uint8_t* row = vp + off[e];
@@ -555,7 +568,7 @@ __device__ __forceinline__ void store_row(const PagedAttnArgs& p, int s, int h, 
 // A unit with more rows has them spread over wr waves side by side (the second
 // and later ones find the codes in the caches); the ATTN_WAVES / wr streams of
 // waves take the tiles in turn.
-template <int D, int MT, bool SPLIT, bool ONCE>
+template <int D, int MT, bool SPLIT, bool ONCE, bool P16>
 __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_attention_kernel(const PagedAttnArgs p) {
   constexpr int KB = D / 4;    // bytes of a key per lane
   constexpr int VB = D / 16;   // bytes of a value per lane, and output tiles
@@ -646,19 +659,19 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
     Pages now, next, ahead;
     Tile<D> x;
     if (t < tb) {
-      find_pages(p, hd, t, true, now);
-      find_pages(p, hd, t + streams, t + streams < tb, next);
-      load_k<D, ONCE>(p, hd, t, now, k_lane, x);
+      find_pages<P16>(p, hd, t, true, now);
+      find_pages<P16>(p, hd, t + streams, t + streams < tb, next);
+      load_k<D, ONCE, P16>(p, hd, t, now, k_lane, x);
     }
     while (t < tb) {
       Scales scl;
-      load_scales(p, hd, now, scl);
-      find_pages(p, hd, t + 2 * streams, t + 2 * streams < tb, ahead);
-      load_v<D, ONCE>(p, hd, t, now, v_lane, x);
+      load_scales<P16>(p, hd, now, scl);
+      find_pages<P16>(p, hd, t + 2 * streams, t + 2 * streams < tb, ahead);
+      load_v<D, ONCE, P16>(p, hd, t, now, v_lane, x);
       f32x4 sc[MT][2];
       scores<D, MT>(x, q, sc);
       __builtin_amdgcn_sched_barrier(0);
-      if (t + streams < tb) load_k<D, ONCE>(p, hd, t + streams, next, k_lane, x);
+      if (t + streams < tb) load_k<D, ONCE, P16>(p, hd, t + streams, next, k_lane, x);
       __builtin_amdgcn_sched_barrier(0);
       const bool whole = t * 32 >= lo_all && t * 32 + 31 <= hi_all && scl.ok[0] && scl.ok[1];
       f16x8 pf[MT];
@@ -865,14 +878,14 @@ AttnPlan attn_plan(int64_t S, int64_t Hkv, int64_t row_tiles, int64_t D, int64_t
 // Workgroups of the join.
 int64_t join_grid(const AttnPlan& a, int64_t S) { return S * a.units * (a.rt * 16 / a.rps); }
 
-template <int D, int MT, bool ONCE>
+template <int D, int MT, bool ONCE, bool P16>
 hipError_t launch(const PagedAttnArgs& p, const AttnPlan& a, hipStream_t stream) {
   if (!a.split) {
-    paged_attention_kernel<D, MT, false, ONCE>
+    paged_attention_kernel<D, MT, false, ONCE, P16>
         <<<dim3((unsigned)((int64_t)p.S * p.units)), dim3(ATTN_THREADS), 0, stream>>>(p);
     return hipGetLastError();
   }
-  paged_attention_kernel<D, MT, true, ONCE><<<dim3((unsigned)p.shares), dim3(ATTN_THREADS), 0, stream>>>(p);
+  paged_attention_kernel<D, MT, true, ONCE, P16><<<dim3((unsigned)p.shares), dim3(ATTN_THREADS), 0, stream>>>(p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   paged_attention_join_kernel<D><<<dim3((unsigned)join_grid(a, p.S)), dim3(ATTN_THREADS), 0, stream>>>(p);
@@ -919,7 +932,8 @@ hipError_t launch_paged_attention(PagedAttnArgs p, hipStream_t stream) {
   const bool once = a.rt == a.mt && p.groups == 1 && 2 * (int64_t)p.S * p.Hkv * seen * p.D >= (int64_t(256) << 20);
 #define ATTN_CASE(D_, MT)                              \
   if (p.D == D_ && a.mt == MT)                         \
-    return once ? launch<D_, MT, true>(p, a, stream) : launch<D_, MT, false>(p, a, stream);
+    return once ? p.P == 16 ? launch<D_, MT, true, true>(p, a, stream) : launch<D_, MT, true, false>(p, a, stream) \
+                : p.P == 16 ? launch<D_, MT, false, true>(p, a, stream) : launch<D_, MT, false, false>(p, a, stream);
   ATTN_CASE(64, 1) ATTN_CASE(64, 2)
   ATTN_CASE(128, 1) ATTN_CASE(128, 2)
   ATTN_CASE(256, 1)
