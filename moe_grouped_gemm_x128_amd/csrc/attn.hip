@@ -27,8 +27,8 @@
 // The weights P are rounded to FP16 (11 bits; rounding them to BF16 would add
 // as much error again as the BF16 output has); to keep them in FP16's range
 // the scale of V is taken into the exponent: with y_t = x_t log2 e + log2 sv_t,
-//   o = sum_t 2^(y_t - M) code_t / sum_t 2^(y_t - M) / sv_t,  M = max y,
-// and P is held times 2^14, so that weights down to 2^-28 of the largest are
+//   o = sum_t 2^(y_t - M) code_t / sum_t 2^(y_t - M) / sv_t,  M = ceil(max y),
+// and P is held times 2^14, so that weights down to 2^-27 of the largest are
 // normal numbers.
 // Sums, maxima and the output stay in FP32.
 //
@@ -69,7 +69,7 @@ constexpr int ATTN_THREADS = 64 * ATTN_WAVES;
 // registers of a lane, the queries D / 8 MT, a tile's codes D / 4.
 constexpr int WAVES_PER_SIMD(int D, int MT) { return D * MT <= 128 ? 3 : 2; }
 constexpr int FEW_TILES = 32;
-constexpr float P_GAIN = 16384.0f;  // weights are held times 2^14 in FP16
+constexpr float P_GAIN = 16384.0f, P_GAIN_LOG2 = 14.0f;  // weights are held times 2^14 in FP16
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
 
 // Four E4M3 codes -> four BF16 values in two words.
@@ -396,25 +396,32 @@ __device__ __forceinline__ void scores(const Tile<D>& x, const bf16x8 (&q)[MT][D
   }
 }
 
+// The larger one; NaN if one is NaN.
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
 // Weights of a tile: the running maxima and sums move on, the outputs so far
 // are scaled to the new maxima; pf gets P^T as the second product wants it.
 // whole: every row sees all 32 positions.
-template <int D, int MT>
+// The maximum is taken up to a whole number (of a power of two): with V's scale
+// a power of two, too, log2 sv + 14 - M is exact, and a weight's exponent takes
+// one rounding, that of the FMA.
+template <int D, int MT, bool P16>
 __device__ __forceinline__ void weigh(const f32x4 (&sc)[MT][2], const Scales& x, const Rows (&r)[MT], bool whole, int t,
                                       int g4, float qk, RowState<D> (&st)[MT], f16x8 (&pf)[MT]) {
   float c[2], lsv[2], inv[2];  // (scales count as 1 where a half takes no part: page 0's may be anything)
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const float vs = __int_as_float(x.ok[u] ? x.vs[u] : 0x3f800000);
-    c[u] = __int_as_float(x.ok[u] ? x.ks[u] : 0x3f800000) * qk;
+    // (positive: a masked score is -inf, and stays it)
+    c[u] = larger(__int_as_float(x.ok[u] ? x.ks[u] : 0x3f800000) * qk, 1.17549435e-38f);
     lsv[u] = __builtin_amdgcn_logf(vs);
-    inv[u] = __builtin_amdgcn_rcpf(vs);
+    inv[u] = __builtin_amdgcn_rcpf(vs) * (1.0f / P_GAIN);
   }
 #pragma unroll
   for (int k = 0; k < MT; ++k) {
     float y[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = sc[k][i / 4][i % 4] * c[i / 4];
+    for (int i = 0; i < 8; ++i) y[i] = sc[k][i / 4][i % 4];
     if (!whole) {
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -422,10 +429,11 @@ __device__ __forceinline__ void weigh(const f32x4 (&sc)[MT][2], const Scales& x,
         y[i] = x.ok[i / 4] && at >= r[k].see_lo && at <= r[k].see_hi ? y[i] : -INFINITY;
       }
     }
-    float mx = fmaxf(fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3])) + lsv[0],
-                     fmaxf(fmaxf(y[4], y[5]), fmaxf(y[6], y[7])) + lsv[1]);
-    mx = quarters(mx, [](float a, float b) { return fmaxf(a, b); });
-    const float m_new = fmaxf(st[k].m, mx);
+    float mx = larger(larger(y[0], y[1]), larger(y[2], y[3])), mx1 = larger(larger(y[4], y[5]), larger(y[6], y[7]));
+    if (P16) mx = larger(__builtin_fmaf(mx, c[0], lsv[0]), __builtin_fmaf(mx1, c[1], lsv[1]));
+    else mx = __builtin_fmaf(larger(mx, mx1), c[0], lsv[0]);
+    mx = __builtin_ceilf(quarters(mx, larger));
+    const float m_new = larger(st[k].m, mx);
     const float m_use = m_new == -INFINITY ? 0.0f : m_new;  // nothing seen so far
     if (__any(m_new != st[k].m)) {  // (seldom, once the largest scores have been seen)
       const float alpha = __builtin_amdgcn_exp2f(st[k].m - m_use);
@@ -436,14 +444,12 @@ __device__ __forceinline__ void weigh(const f32x4 (&sc)[MT][2], const Scales& x,
 #pragma unroll
         for (int e = 0; e < 4; ++e) st[k].o[i][e] *= alpha;
     }
-    // (log2 sv - M is exact where it matters, near the largest weight, so that
-    // a weight and the sum are as exact as the score)
-    const float d[2] = {lsv[0] - m_use, lsv[1] - m_use};
+    const float d[2] = {lsv[0] + P_GAIN_LOG2 - m_use, lsv[1] + P_GAIN_LOG2 - m_use};
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float w = __builtin_amdgcn_exp2f(y[i] + d[i / 4]);
+      const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(y[i], c[i / 4], d[i / 4]));
       st[k].l = __builtin_fmaf(w, inv[i / 4], st[k].l);
-      pf[k][i] = (_Float16)(w * P_GAIN);
+      pf[k][i] = (_Float16)w;
     }
   }
 }
@@ -499,18 +505,13 @@ __device__ __forceinline__ void clear_values(const Scales& place, int t, int g4,
 template <int D, int MT>
 __device__ __forceinline__ void take_out_nans(const Scales& place, const Rows (&r)[MT], int t, int g4, Tile<D>& x,
                                               RowState<D> (&st)[MT]) {
-  Tile<D> places;  // code 1 (a positive value) where there is a NaN
+  // code 1 (a positive value) where there is a NaN
+  const auto nans = [](int w) { return (int)(((((uint32_t)w & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u); };
   int hit = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i)
 #pragma unroll
-    for (int b = 0; b < D / 64; ++b) {
-      int& w = x.v[i / 4][i % 4][b];
-      const int n = (int)(((((uint32_t)w & 0x7f7f7f7fu) + 0x01010101u) >> 7) & 0x01010101u);
-      places.v[i / 4][i % 4][b] = n;
-      hit |= n;
-      w &= (int)~((uint32_t)n * 0xffu);
-    }
+    for (int b = 0; b < D / 64; ++b) hit |= nans(x.v[i / 4][i % 4][b]);
   if (!__any(hit != 0)) return;
   f16x8 sees[MT];
 #pragma unroll
@@ -522,8 +523,16 @@ __device__ __forceinline__ void take_out_nans(const Scales& place, const Rows (&
     }
 #pragma unroll
   for (int b = 0; b < D / 32; ++b) {
+    Tile<64> places;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      int& w = x.v[i / 4][i % 4][b / 2];
+      const int n = nans(w) & (b % 2 == 0 ? 0x0000ffff : (int)0xffff0000);  // elements 2 b and 2 b + 1
+      places.v[i / 4][i % 4][0] = n;
+      w &= (int)~((uint32_t)n * 0xffu);
+    }
     f16x8 v0, v1;
-    turn_values<D>(places, b, v0, v1);
+    turn_values<64>(places, b % 2, v0, v1);
 #pragma unroll
     for (int k = 0; k < MT; ++k) {
       const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
@@ -583,7 +592,7 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
   const int r16 = lane & 15, g4 = lane >> 4;
   const uint32_t k_lane = (uint32_t)(r16 * p.skc_t + g4 * 16);
   const uint32_t v_lane = (uint32_t)(4 * g4 * p.svc_t + r16 * VB);
-  const float qk = p.scale * LOG2E;
+  const float qk = fabsf(p.scale) * LOG2E;  // (its sign goes into the queries)
   const int streams = uniform(ATTN_WAVES / p.wr), stream = uniform(wave / p.wr), wgroup = wave - stream * p.wr;
 
   Share line = {0, 1, 0, 1, 0, 0, 0};
@@ -663,6 +672,13 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
       find_pages<P16>(p, hd, t + streams, t + streams < tb, next);
       load_k<D, ONCE, P16>(p, hd, t, now, k_lane, x);
     }
+    if (p.scale < 0.0f) {
+#pragma unroll
+      for (int k = 0; k < MT; ++k)
+#pragma unroll
+        for (int j = 0; j < D / 32; ++j)
+          q[k][j] = __builtin_bit_cast(bf16x8, __builtin_bit_cast(i32x4, q[k][j]) ^ (int)0x80008000);
+    }
     while (t < tb) {
       Scales scl;
       load_scales<P16>(p, hd, now, scl);
@@ -675,7 +691,7 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
       __builtin_amdgcn_sched_barrier(0);
       const bool whole = t * 32 >= lo_all && t * 32 + 31 <= hi_all && scl.ok[0] && scl.ok[1];
       f16x8 pf[MT];
-      weigh<D, MT>(sc, scl, r, whole, t, g4, qk, st, pf);
+      weigh<D, MT, P16>(sc, scl, r, whole, t, g4, qk, st, pf);
       if (!whole) {
         clear_values<D>(scl, t, g4, lo_any, hi_any, x);
         if (qi_first != qi_last) take_out_nans<D, MT>(scl, r, t, g4, x, st);
