@@ -93,6 +93,13 @@ __device__ __forceinline__ void local_barrier() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// The kernel's arguments, to be fetched where they are used.
+__device__ __forceinline__ const PagedAttnArgs& arguments() {
+  auto p = (const __attribute__((address_space(4))) PagedAttnArgs*)__builtin_amdgcn_kernarg_segment_ptr();
+  asm volatile("" : "+s"(p));
+  return *(const PagedAttnArgs*)p;
+}
+
 // Tiles of 32 positions that the queries of sequence s look at: [begin, end).
 // A sequence whose queries see nothing has one tile (of masked positions), so
 // that every unit is somebody's work.
@@ -702,6 +709,9 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
       t += streams;
     }
 
+    // (a cut kernel fetches the arguments of this part again: kept over the tiles
+    // they would be spilled, 0.5 us of a call)
+    const PagedAttnArgs& pe = SPLIT ? arguments() : p;
     // join the waves: each scales its output to the common maximum, then every
     // thread sums four columns of a row
     if (SPLIT) local_barrier();  // the last piece's join has been read
@@ -715,14 +725,14 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
     }
     local_barrier();
     const bool piece = t0 > 0 || t1 < nt;
-    float* part = piece ? part_at<D>(p, 2 * (int64_t)blockIdx.x + (t0 == 0)) : nullptr;
+    float* part = piece ? part_at<D>(pe, 2 * (int64_t)blockIdx.x + (t0 == 0)) : nullptr;
 #pragma unroll
     for (int k = 0; k < MT; ++k) {
-      if (row0 + 16 * k >= p.rows) break;
+      if (row0 + 16 * k >= pe.rows) break;
       float m = -INFINITY, l = 0.0f;
-      for (int w = wgroup; w < ATTN_WAVES; w += p.wr) m = fmaxf(m, sm[k][w][r16]);
+      for (int w = wgroup; w < ATTN_WAVES; w += pe.wr) m = fmaxf(m, sm[k][w][r16]);
       // (without a maximum the sums are 0, or NaN where every score is NaN)
-      for (int w = wgroup; w < ATTN_WAVES; w += p.wr)
+      for (int w = wgroup; w < ATTN_WAVES; w += pe.wr)
         l += sl[k][w][r16] * (sm[k][w][r16] == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(sm[k][w][r16] - m));
       const float f = st[k].m == -INFINITY ? 1.0f : __builtin_amdgcn_exp2f(st[k].m - m);
       if (k > 0) local_barrier();  // the last row tile's sums have been read
@@ -740,13 +750,13 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
       local_barrier();
       constexpr int TAKE = D / 64;  // of the row tile's D / 4 x 16 quadruples
       f32x4 sum[TAKE];
-      for (int g = 0; g < p.wr; ++g) {
+      for (int g = 0; g < pe.wr; ++g) {
 #pragma unroll
         for (int i = 0; i < TAKE; ++i) {
           const int j = threadIdx.x + i * ATTN_THREADS, c = j % (D / 4) * 4, rw = j / (D / 4);
           sum[i] = *reinterpret_cast<const f32x4*>(&so[g][rw][c]);
         }
-        for (int w = g + p.wr; w < ATTN_WAVES; w += p.wr)
+        for (int w = g + pe.wr; w < ATTN_WAVES; w += pe.wr)
 #pragma unroll
           for (int i = 0; i < TAKE; ++i) {
             const int j = threadIdx.x + i * ATTN_THREADS, c = j % (D / 4) * 4, rw = j / (D / 4);
@@ -757,22 +767,22 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
 #pragma unroll
         for (int i = 0; i < TAKE; ++i) {
           const int j = threadIdx.x + i * ATTN_THREADS, c = j % (D / 4) * 4, rw = j / (D / 4), rr = (g * MT + k) * 16 + rw;
-          if (row0 + rr >= p.rows) continue;
+          if (row0 + rr >= pe.rows) continue;
           if (SPLIT && piece) {
             *reinterpret_cast<f32x4*>(part + rr * D + c) = sum[i];
             if (c == 0) {
-              part[p.rt * 16 * D + rr] = row_m[g][rw];
-              part[p.rt * 16 * (D + 1) + rr] = row_l[g][rw];
+              part[pe.rt * 16 * D + rr] = row_m[g][rw];
+              part[pe.rt * 16 * (D + 1) + rr] = row_l[g][rw];
             }
           } else {
-            store_row<D>(p, s, h, row0 + rr, c, sum[i], row_m[g][rw], row_l[g][rw]);
+            store_row<D>(pe, s, h, row0 + rr, c, sum[i], row_m[g][rw], row_l[g][rw]);
           }
         }
       }
     }
     if (!SPLIT) return;
     if (t0 == 0 && threadIdx.x == 0) {
-      int32_t* parts = unit_parts(p, (int64_t)s * p.units + unit);
+      int32_t* parts = unit_parts(pe, (int64_t)s * pe.units + unit);
       parts[0] = blockIdx.x;
       parts[1] = (line.at + nt - 1) / line.size;
     }
