@@ -868,16 +868,23 @@ AttnPlan attn_plan(int64_t S, int64_t Hkv, int64_t row_tiles, int64_t D, int64_t
   a.rt = a.mt * a.wr;
   a.units = (int)(Hkv * ((row_tiles + a.rt - 1) / a.rt));
   const int64_t cap_tiles = (cap + 31) / 32, units = S * a.units;
-  // Short caches are not cut, the longer the more units there are to fill the
-  // machine: the cut costs the scans of the lengths and the join's launch, 3 to
-  // 10 us.  Not cut / cut, in us (cache capacity; lengths from half of it up;
-  // D = 128): 8 units: 1024 tokens 10.5 / 10.4, 2048 tokens 16.6 / 10.9;
-  // 128 units: 2048 tokens 19.8 / 22.7, 4096 tokens 33.9 / 29.8;
-  // 512 units: 2048 tokens 41 / 48, 4096 tokens 76 / 82, 8192 tokens 151 / 144;
-  // 1024 units of lengths from 1 to 8192: 279 / 204.
-  const int64_t direct = 32 + units / 4;
+  // Short caches are not cut: the cut costs the shares' search, the parts and the
+  // join's launch, 3 to 10 us.  How short depends on what a unit's streams of
+  // waves do in that time, and the more units there are to fill the machine, the
+  // longer.  Not cut / cut, in us (units, cache capacity; lengths from half of it up):
+  //   D = 128, four streams: 8 units, 1024 tokens 9.8 / 10.6, 2048 15.2 / 10.7;
+  //     128 units, 2048 18.9 / 18.9, 4096 32.1 / 25.7; 512 units, 2048 41 / 48,
+  //     4096 76 / 79, 8192 148 / 142; 1024 units of 1 to 8192 tokens 279 / 203
+  //   D = 128, two streams (64 rows): 16 units, 256 tokens 11.6 / 14.5, 512 15.4 /
+  //     15.1, 1024 22.5 / 16.8; 128 units, 1024 24.1 / 28.7, 2048 38.1 / 30.8
+  //   D = 256, two streams (32 rows): 16 units, 512 tokens 16.3 / 14.0, 1024 24.6 /
+  //     16.0; 64 units, 512 16.9 / 17.0, 1024 26.0 / 19.8; 256 units, 2048 57.6 / 69
+  //   D = 256, four streams: 16 units, 512 tokens 9.8 / 12.4, 1024 14.1 / 11.7; 128
+  //     units, 1024 16.0 / 20.8, 2048 25.4 / 28.2 (here the rule cuts a little early)
+  const int64_t streams = ATTN_WAVES / a.wr;
+  const int64_t direct = streams * (D > 128 ? 4 : 8) + units / 4;
   a.split = cap_tiles > (direct < 128 ? direct : 128);
-  a.min_share = ATTN_WAVES / a.wr;  // a tile for each stream
+  a.min_share = (int)streams;  // a tile for each
   // Shares: two workgroups a compute unit, resident at once, so that all end
   // together (its registers would hold a third at D <= 128).  256 / 512 / 768 /
   // 1024 shares, in us, at D = 128: 128 sequences up to 8192 long, 8 heads 226 /
