@@ -27,8 +27,8 @@
 // The weights P are rounded to FP16 (11 bits; rounding them to BF16 would add
 // as much error again as the BF16 output has); to keep them in FP16's range
 // the scale of V is taken into the exponent: with y_t = x_t log2 e + log2 sv_t,
-//   o = sum_t 2^(y_t - M) code_t / sum_t 2^(y_t - M) / sv_t,  M = ceil(max y),
-// and P is held times 2^14, so that weights down to 2^-27 of the largest are
+//   o = sum_t 2^(y_t - M) code_t / sum_t 2^(y_t - M) / sv_t,  M = max y,
+// and P is held times 2^14, so that weights down to 2^-28 of the largest are
 // normal numbers.
 // Sums, maxima and the output stay in FP32.
 //
@@ -70,6 +70,7 @@ constexpr int ATTN_THREADS = 64 * ATTN_WAVES;
 constexpr int WAVES_PER_SIMD(int D, int MT) { return D * MT <= 128 ? 3 : 2; }
 constexpr int FEW_TILES = 32;
 constexpr float P_GAIN = 16384.0f, P_GAIN_LOG2 = 14.0f;  // weights are held times 2^14 in FP16
+constexpr float ON_GRID = 192.0f;  // added and taken off: leaves a multiple of 2^-16
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
 
 // Four E4M3 codes -> four BF16 values in two words.
@@ -409,9 +410,10 @@ __device__ __forceinline__ float larger(float a, float b) { return __builtin_ele
 // Weights of a tile: the running maxima and sums move on, the outputs so far
 // are scaled to the new maxima; pf gets P^T as the second product wants it.
 // whole: every row sees all 32 positions.
-// The maximum is taken up to a whole number (of a power of two): with V's scale
-// a power of two, too, log2 sv + 14 - M is exact, and a weight's exponent takes
-// one rounding, that of the FMA.
+// The maximum is rounded to a multiple of 2^-16 (of coarser powers past 64): so
+// log2 sv + 14 - M is exact, V's scale being a power of two, and a weight's
+// exponent takes one rounding, that of the FMA; and the largest weight is 2^14
+// nearly enough to stay that in FP16, which matters to rows with few others.
 template <int D, int MT, bool P16>
 __device__ __forceinline__ void weigh(const f32x4 (&sc)[MT][2], const Scales& x, const Rows (&r)[MT], bool whole, int t,
                                       int g4, float qk, RowState<D> (&st)[MT], f16x8 (&pf)[MT]) {
@@ -439,7 +441,7 @@ __device__ __forceinline__ void weigh(const f32x4 (&sc)[MT][2], const Scales& x,
     float mx = larger(larger(y[0], y[1]), larger(y[2], y[3])), mx1 = larger(larger(y[4], y[5]), larger(y[6], y[7]));
     if (P16) mx = larger(__builtin_fmaf(mx, c[0], lsv[0]), __builtin_fmaf(mx1, c[1], lsv[1]));
     else mx = __builtin_fmaf(larger(mx, mx1), c[0], lsv[0]);
-    mx = __builtin_ceilf(quarters(mx, larger));
+    mx = quarters(mx, larger) + ON_GRID - ON_GRID;
     const float m_new = larger(st[k].m, mx);
     const float m_use = m_new == -INFINITY ? 0.0f : m_new;  // nothing seen so far
     if (__any(m_new != st[k].m)) {  // (seldom, once the largest scores have been seen)
