@@ -43,11 +43,11 @@
 // 80 scalar instructions (D = 128), 0.68 us to a wave alone; four waves on
 // each of two workgroups a compute unit keep 64 KiB of codes on their way there
 // and reach what HBM gives to reads: 128 sequences of 1 to 8192 tokens (8 KV
-// heads, D = 128, 1.09 GB) 197 us, 5.5 TB/s; 4 of 60,000 to 131,071 (4 heads, 410
-// MB) 69 us, 5.9 TB/s.  Calls with little to read are bound by what each share
+// heads, D = 128, 1.09 GB) 193 us, 5.6 TB/s; 4 of 60,000 to 131,071 (4 heads, 410
+// MB) 68 us, 6.0 TB/s.  Calls with little to read are bound by what each share
 // spends before and after its tiles, 3 and 2 us, the first tile's 2 to 5 us of
 // latency, and the join's launch, 4 to 6 us: 32 sequences, window 2048, four
-// queries of 8 heads each over 2 KV heads, D = 256 (65 MB): 24 + 4.1 us; one
+// queries of 8 heads each over 2 KV heads, D = 256 (65 MB): 23 + 4.2 us; one
 // sequence of 777 tokens, not cut: 9.8 us.
 
 #include "common.hpp"
