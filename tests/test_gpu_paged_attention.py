@@ -224,6 +224,42 @@ def test_scales_far_apart():
     _compare(c, out, lse, 0.1, 0, "scales")
 
 
+@pytest.mark.parametrize("scale,lens,P", [(0.0, [70, 3, 0], 32), (0.0, [4000, 45, 1], 64), (-0.0, [40, 17, 2], 16)])
+def test_a_scale_of_zero_weighs_all_alike(scale, lens, P):
+    say(f"paged_attention_fp8 scale {scale} lens={lens} P={P}")
+    c = _case(41, 3, 3, 4, 2, 64, P, lens)
+    out, lse = _run(c, scale, 30)
+    _compare(c, out, lse, scale, 30, "zero scale")
+    seen = np.array([[min(30, max(0, ln - 3 + i + 1)) for i in range(3)] for ln in lens])[:, :, None]
+    with np.errstate(divide="ignore"):
+        want = np.broadcast_to(np.log(seen.astype(np.float64)), lse.shape)
+    assert np.array_equal(np.isinf(lse), np.isinf(want))
+    some = np.isfinite(want)
+    assert np.all(np.abs(lse[some] - want[some]) <= 1e-5)
+
+
+@pytest.mark.parametrize("D,P,lens", [(128, 64, [900, 31]), (256, 16, [200, 17]), (64, 32, [5000, 3000])])
+def test_scales_that_are_no_powers_of_two(D, P, lens):
+    say(f"paged_attention_fp8 odd scales D={D} P={P} lens={lens}")
+    c = _case(51 + D, 2, 2, 8, 2, D, P, lens)
+    rng = np.random.default_rng(5)
+    for x in ("ks", "vs"):
+        c[x] = (c[x] * rng.uniform(1.0, 2.0, size=c[x].shape)).astype(np.float32)
+    c["dev"][2:] = [to_dev(c["ks"]), to_dev(c["vs"])]
+    out, lse = _run(c, 0.09)
+    _compare(c, out, lse, 0.09, 0, "odd scales")
+
+
+def test_one_weight_above_all():
+    """Queries so sharp that a row is one position, or a few: scores of
+    hundreds, up and down."""
+    say("paged_attention_fp8 sharp rows")
+    for scale in (1.0, -1.0):
+        c = _case(61, 2, 2, 8, 2, 128, 64, [700, 90], sharp=4.0)
+        out, lse = _run(c, scale)
+        _compare(c, out, lse, scale, 0, "sharp")
+
+
 def test_nan_where_nothing_looks():
     """A NaN value at the newest position of a draft spoils only the queries
     that see it; before a window, none."""
