@@ -71,6 +71,7 @@ constexpr int WAVES_PER_SIMD(int D, int MT) { return D * MT <= 128 ? 3 : 2; }
 constexpr int FEW_TILES = 32;
 constexpr float P_GAIN = 16384.0f, P_GAIN_LOG2 = 14.0f;  // weights are held times 2^14 in FP16
 constexpr float ON_GRID = 192.0f;  // added and taken off: leaves a multiple of 2^-16
+constexpr float FAR = 65536.0f;    // of a maximum in base 2: from here on exponents are rounded before the maximum goes off
 constexpr float LOG2E = 1.44269504088896340736f, LN2 = 0.69314718055994530942f;
 
 // Four E4M3 codes -> four BF16 values in two words.
@@ -414,6 +415,10 @@ __device__ __forceinline__ float larger(float a, float b) { return __builtin_ele
 // log2 sv + 14 - M is exact, V's scale being a power of two, and a weight's
 // exponent takes one rounding, that of the FMA; and the largest weight is 2^14
 // nearly enough to stay that in FP16, which matters to rows with few others.
+// A maximum past FAR stays as it is, and the exponents are rounded as it was, so
+// that the largest is 14 again: from scores of 2^24 on FP32's spacing is 2 and
+// more, and exponents rounded in another way could pass FP16's range, or all
+// fall below it.
 template <int D, int MT, bool P16>
 __device__ __forceinline__ void weigh(const f32x4 (&sc)[MT][2], const Scales& x, const Rows (&r)[MT], bool whole, int t,
                                       int g4, float qk, RowState<D> (&st)[MT], f16x8 (&pf)[MT]) {
@@ -441,11 +446,10 @@ __device__ __forceinline__ void weigh(const f32x4 (&sc)[MT][2], const Scales& x,
     float mx = larger(larger(y[0], y[1]), larger(y[2], y[3])), mx1 = larger(larger(y[4], y[5]), larger(y[6], y[7]));
     if (P16) mx = larger(__builtin_fmaf(mx, c[0], lsv[0]), __builtin_fmaf(mx1, c[1], lsv[1]));
     else mx = __builtin_fmaf(larger(mx, mx1), c[0], lsv[0]);
-    mx = quarters(mx, larger) + ON_GRID - ON_GRID;
-    const float m_new = larger(st[k].m, mx);
-    const float m_use = m_new == -INFINITY ? 0.0f : m_new;  // nothing seen so far
-    if (__any(m_new != st[k].m)) {  // (seldom, once the largest scores have been seen)
-      const float alpha = __builtin_amdgcn_exp2f(st[k].m - m_use);
+    mx = quarters(mx, larger);
+    if (__any(!(mx <= st[k].m))) {  // (seldom, once the largest scores have been seen)
+      const float m_new = larger(st[k].m, fabsf(mx) > FAR ? mx : mx + ON_GRID - ON_GRID);
+      const float alpha = __builtin_amdgcn_exp2f(st[k].m - (m_new == -INFINITY ? 0.0f : m_new));
       st[k].m = m_new;
       st[k].l *= alpha;
 #pragma unroll
@@ -453,10 +457,23 @@ __device__ __forceinline__ void weigh(const f32x4 (&sc)[MT][2], const Scales& x,
 #pragma unroll
         for (int e = 0; e < 4; ++e) st[k].o[i][e] *= alpha;
     }
-    const float d[2] = {lsv[0] + P_GAIN_LOG2 - m_use, lsv[1] + P_GAIN_LOG2 - m_use};
+    const float m_use = st[k].m == -INFINITY ? 0.0f : st[k].m;  // nothing seen so far
+    float x2[8];  // exponents
+    if (__any(fabsf(m_use) > FAR)) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        x2[i] = __builtin_fmaf(y[i], c[i / 4], lsv[i / 4]);
+        asm volatile("" : "+v"(x2[i]));  // (rounded here)
+        x2[i] = (x2[i] - m_use) + P_GAIN_LOG2;
+      }
+    } else {
+      const float d[2] = {lsv[0] + P_GAIN_LOG2 - m_use, lsv[1] + P_GAIN_LOG2 - m_use};
+#pragma unroll
+      for (int i = 0; i < 8; ++i) x2[i] = __builtin_fmaf(y[i], c[i / 4], d[i / 4]);
+    }
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float w = __builtin_amdgcn_exp2f(__builtin_fmaf(y[i], c[i / 4], d[i / 4]));
+      const float w = __builtin_amdgcn_exp2f(x2[i]);
       st[k].l = __builtin_fmaf(w, inv[i / 4], st[k].l);
       pf[k][i] = (_Float16)w;
     }
