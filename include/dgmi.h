@@ -475,8 +475,8 @@ int kv_append_fp8(const dg_tensor* k, const dg_tensor* v, const dg_tensor* k_cac
  *   q         BF16 [S, n, Hq, D]; out BF16, the same shape.  Strides multiples
  *             of 8 elements, 16-byte aligned bases
  *   caches, scales, block_table  as kv_append_fp8; Hq a multiple of Hkv (query
- *             heads h * Hq / Hkv .. share KV head h).  Scales are positive
- *             and finite
+ *             heads h * Hq / Hkv .. share KV head h).  Scales of pages that
+ *             a query sees are positive and finite
  *   seq_lens  I32 [S]: tokens in the cache, the n queries' own included (cut
  *             to what the block table holds).  Query i stands at position
  *             seq_lens[s] - n + i
@@ -488,8 +488,8 @@ int kv_append_fp8(const dg_tensor* k, const dg_tensor* v, const dg_tensor* k_cac
  *   scale     factor of the scores
  *   window    a query sees the window positions up to its own; 0: all of them
  * Positions past a query's own or before its window, and pages outside
- * [0, pages), take no part, whatever their memory holds (NaN codes too).  A
- * query that sees nothing gives 0, with lse -inf.  Weights are rounded to FP16
+ * [0, pages), take no part, whatever their memory holds (NaN codes too, and
+ * the scales of pages that no query sees).  A query that sees nothing gives 0, with lse -inf.  Weights are rounded to FP16
  * on their way into the second product, sums and output accumulate in FP32.
  * The result does not depend on the order in which workgroups run.
  */

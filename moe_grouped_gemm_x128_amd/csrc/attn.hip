@@ -280,13 +280,16 @@ __device__ __forceinline__ const uint8_t* half_at(const PagedAttnArgs& p, const 
   return base + page_offset(page_of<P16>(p, x, u, &ok), page_step) + slot * step;
 }
 
-// The scales of a tile's halves as they are stored.
+// The scales of a tile's halves as they are stored.  ok: the half takes part --
+// its page is there, and where it has a page of its own some row of the wave
+// sees into it ([lo, hi]): the scales of a page that no row sees may be anything.
 struct Scales {
   int ks[2], vs[2];
   bool ok[2];
 };
 template <bool P16>
-__device__ __forceinline__ void load_scales(const PagedAttnArgs& p, const Heads& hd, const Pages& pages, Scales& x) {
+__device__ __forceinline__ void load_scales(const PagedAttnArgs& p, const Heads& hd, const Pages& pages, int t, int lo, int hi,
+                                            Scales& x) {
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     if (!P16 && u == 1) {
@@ -298,6 +301,7 @@ __device__ __forceinline__ void load_scales(const PagedAttnArgs& p, const Heads&
     const int page = page_of<P16>(p, pages, u, &x.ok[u]);
     x.ks[u] = uniform_load(reinterpret_cast<const int32_t*>(reinterpret_cast<const uint8_t*>(hd.ks) + page_offset(page, p.sks_p)));
     x.vs[u] = uniform_load(reinterpret_cast<const int32_t*>(reinterpret_cast<const uint8_t*>(hd.vs) + page_offset(page, p.svs_p)));
+    if (P16) x.ok[u] = x.ok[u] && t * 32 + 16 * u + 15 >= lo && t * 32 + 16 * u <= hi;
   }
 }
 
@@ -422,7 +426,7 @@ __device__ __forceinline__ float larger(float a, float b) { return __builtin_ele
 template <int D, int MT, bool P16>
 __device__ __forceinline__ void weigh(const f32x4 (&sc)[MT][2], const Scales& x, const Rows (&r)[MT], bool whole, int t,
                                       int g4, float qk, RowState<D> (&st)[MT], f16x8 (&pf)[MT]) {
-  float c[2], lsv[2], inv[2];  // (scales count as 1 where a half takes no part: page 0's may be anything)
+  float c[2], lsv[2], inv[2];  // (scales count as 1 where a half takes no part)
 #pragma unroll
   for (int u = 0; u < 2; ++u) {
     const float vs = __int_as_float(x.ok[u] ? x.vs[u] : 0x3f800000);
@@ -707,7 +711,7 @@ __global__ __launch_bounds__(ATTN_THREADS, WAVES_PER_SIMD(D, MT)) void paged_att
     }
     while (t < tb) {
       Scales scl;
-      load_scales<P16>(p, hd, now, scl);
+      load_scales<P16>(p, hd, now, t, lo_any, hi_any, scl);
       find_pages<P16>(p, hd, t + 2 * streams, t + 2 * streams < tb, ahead);
       load_v<D, ONCE, P16>(p, hd, t, now, v_lane, x);
       f32x4 sc[MT][2];
