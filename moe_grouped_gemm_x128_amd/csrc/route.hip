@@ -287,7 +287,8 @@ __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_route_topk_kernel(const
   }
   float wgt;
   if (!p.softmax) {
-    wgt = p.renorm ? __fdiv_rn(z, lanes_sum<LT>(z) + 1e-20f) : z;
+    const float d = p.renorm ? lanes_sum<LT>(z) + 1e-20f : 1.0f;
+    wgt = p.renorm && got ? __fdiv_rn(z, d) : z;  // (0 where nothing was chosen, also beside a NaN)
   } else if (!p.renorm) {
     wgt = got ? __fdiv_rn(z, sum) : 0.0f;
   } else {
