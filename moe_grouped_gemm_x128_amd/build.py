@@ -39,9 +39,11 @@ COMMON_FLAGS = [
     f"-I{CSRC}",
 ]
 
-# flags of single sources: the append's rotation rounds every product and sum
-# on its own (contraction pragmas do not bind under -ffp-contract=fast)
-EXTRA_FLAGS = {"kvcache.hip": ["-ffp-contract=off"]}
+# flags of single sources (contraction pragmas do not bind under -ffp-contract=fast):
+# the append's rotation rounds every product and sum on its own; the routing calls
+# expf, whose own steps must not be fused (its correction for the rounding of x
+# log2 e would count twice: 24 u of the result at x = -40 instead of 1.4)
+EXTRA_FLAGS = {"kvcache.hip": ["-ffp-contract=off"], "route.hip": ["-ffp-contract=off"]}
 
 
 def _compile(src):

@@ -35,3 +35,24 @@ def test_no_expert_no_weight():
             assert i.tolist() == [[30, 7, -1, -1], [3, -1, -1, -1], [5, 6, -1, -1]], (score, renorm)
             assert np.all(v[i == -1] == 0), (score, renorm, v.tolist())
             assert np.isnan(v[0, 1]) and np.isnan(v[1, 0]) and np.all(np.isfinite(v[2]))
+
+
+@pytest.mark.parametrize("T", [300, 2100, 8200])  # 64, 32 and 16 lanes a token
+def test_scores_over_the_range_of_the_exponential(T):
+    """One expert's sigmoid and a softmax of two, the larger logit 0: the
+    exponential within an ulp (2 u), its sum with 1 and the quotient u each:
+    4 u of the score, whatever the logit."""
+    say(f"moe_route_topk scores over the range of the exponential T={T}")
+    x = np.linspace(-80, 80, T).astype(np.float32)[:, None]
+    d, xv = _logits(x, False)
+    _, w = _route(d, 1, score="sigmoid", renormalize=False)
+    ref = 1 / (1 + np.exp(-xv))
+    err = np.abs(w.cpu().numpy() - ref)
+    assert np.all(err <= 4 * U * ref), f"sigmoid: {np.max(err / ref) / U} u at {xv[np.argmax(err / ref)]}"
+    d, xv = _logits(np.concatenate([np.zeros_like(x), -np.abs(x)], axis=1), False)
+    ref = np.exp(xv) / (1 + np.exp(xv[:, 1:]))
+    for renorm in (True, False):
+        idx, w = _route(d, 2, score="softmax", renormalize=renorm)
+        want = np.take_along_axis(ref, idx.cpu().numpy().astype(np.int64), 1)
+        err = np.abs(w.cpu().numpy() - want)
+        assert np.all(err <= 4 * U * want), f"softmax: {np.max(err / want) / U} u"
