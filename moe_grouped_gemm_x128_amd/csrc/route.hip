@@ -338,7 +338,8 @@ __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_route_topk_bwd_kernel(c
       const float D = lanes_sum<LT>(z) + 1e-20f;
       dz = __fdiv_rn(g - __fdiv_rn(lanes_sum<LT>(g * z), D), D);
     }
-    d = idx >= 0 ? dz * (z * (1.0f - z)) : 0.0f;
+    // (1 - s(x) as s(-x): taken from the rounded s it would be 0 from logits of 17 on)
+    d = idx >= 0 ? dz * (z * sigmoid_f32(-xz)) : 0.0f;
   } else if (p.renorm) {
     const float m = lanes_max<LT>(xz);
     const float e = idx >= 0 ? expf(xz - m) : 0.0f;

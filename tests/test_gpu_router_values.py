@@ -56,3 +56,23 @@ def test_scores_over_the_range_of_the_exponential(T):
         want = np.take_along_axis(ref, idx.cpu().numpy().astype(np.int64), 1)
         err = np.abs(w.cpu().numpy() - want)
         assert np.all(err <= 4 * U * want), f"softmax: {np.max(err / want) / U} u"
+
+
+@pytest.mark.parametrize("T,E,k,bf16", [(64, 40, 20, False), (200, 256, 8, False), (33, 64, 6, True)])
+def test_gradient_of_confident_sigmoid_experts(T, E, k, bf16):
+    """dx = g scale s(x) s(-x): two sigmoids and three products, at most 12 u of
+    itself, from logits of -40 to 40, where 1 - s is far below FP32's spacing at 1."""
+    say(f"moe_route_topk_bwd confident sigmoid T={T} E={E} k={k}")
+    rng = np.random.default_rng(60 + E)
+    x = rng.uniform(-40, 40, size=(T, E)).astype(np.float32)
+    x[0] = np.linspace(8, 30, E)
+    idx = np.argsort(rng.uniform(size=(T, E)), axis=1)[:, :k].astype(np.int32)
+    g = rng.normal(size=(T, k)).astype(np.float32)
+    d, xv = _logits(x, bf16)
+    out = torch.empty(T, E, device="cuda")
+    _mg().moe_route_topk_bwd(d, to_dev(idx), to_dev(g), out, score="sigmoid", renormalize=False, scale=1.5)
+    ref = np.zeros((T, E))
+    z = np.take_along_axis(xv, idx.astype(np.int64), 1)
+    np.put_along_axis(ref, idx.astype(np.int64), 1.5 * g.astype(np.float64) / (1 + np.exp(-z)) / (1 + np.exp(z)), 1)
+    err = np.abs(out.cpu().numpy() - ref)
+    assert np.all(err <= 12 * U * np.abs(ref)), f"largest relative error {np.max(err / np.maximum(np.abs(ref), 1e-300))}"
