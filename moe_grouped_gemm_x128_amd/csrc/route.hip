@@ -305,6 +305,15 @@ __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_route_topk_kernel(const
   }
 }
 
+// g less its mean under weights q of sum 1.  The mean goes off in two steps, r as
+// it was rounded and then the mean of what is left: where one weight is nearly 1
+// its g - mean is far below the spacing of g and would be lost in one.
+template <int LT>
+__device__ __forceinline__ float less_mean(float g, float q, float r) {
+  const float left = g - r;
+  return left - lanes_sum<LT>(left * q);
+}
+
 template <int LT, int NE>
 __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_route_topk_bwd_kernel(const RouteTopkBwdArgs p) {
   constexpr int TOKENS = 64 * ROUTER_WAVES / LT;
@@ -327,16 +336,15 @@ __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_route_topk_bwd_kernel(c
     xz = p.bf16 ? bf16_to_f32(static_cast<const uint16_t*>(p.logits)[row + idx])
                 : static_cast<const float*>(p.logits)[row + idx];
   }
-  float d = 0.0f;    // gradient of logit idx through choice `lane`
-  float x[NE], sub = 0.0f;  // softmax scores of the row, and what each takes off
-#pragma unroll
-  for (int i = 0; i < NE; ++i) x[i] = 0.0f;
+  float d = g;      // gradient of logit idx through choice `lane`; softmax weights as they are: of its score
+  float x[NE], r = 0.0f;  // softmax scores of the row, and the mean of their gradients
   if (!p.softmax) {
     const float z = idx >= 0 ? sigmoid_f32(xz) : 0.0f;
     float dz = g;
     if (p.renorm) {
-      const float D = lanes_sum<LT>(z) + 1e-20f;
-      dz = __fdiv_rn(g - __fdiv_rn(lanes_sum<LT>(g * z), D), D);
+      // (the weights z / D add up to 1 - 1e-20 / D)
+      const float D = lanes_sum<LT>(z) + 1e-20f, q = __fdiv_rn(z, D), mean = lanes_sum<LT>(g * q);
+      dz = __fdiv_rn(less_mean<LT>(g, q, mean) + mean * __fdiv_rn(1e-20f, D), D);
     }
     // (1 - s(x) as s(-x): taken from the rounded s it would be 0 from logits of 17 on)
     d = idx >= 0 ? dz * (z * sigmoid_f32(-xz)) : 0.0f;
@@ -345,7 +353,7 @@ __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_route_topk_bwd_kernel(c
     const float e = idx >= 0 ? expf(xz - m) : 0.0f;
     const float sum = lanes_sum<LT>(e);
     const float q = idx >= 0 ? __fdiv_rn(e, sum) : 0.0f;
-    d = q * (g - lanes_sum<LT>(g * q));
+    d = q * less_mean<LT>(g, q, lanes_sum<LT>(g * q));
   } else {
     load_run<NE>(p.logits, p.bf16, row + e0, n, p.vec, -INFINITY, x);
     float top = -INFINITY, sum = 0.0f;
@@ -363,20 +371,30 @@ __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_route_topk_bwd_kernel(c
 #pragma unroll
     for (int i = 0; i < NE; ++i) x[i] = __fdiv_rn(x[i], sum);
     const float z = idx >= 0 ? __fdiv_rn(expf(xz - top), sum) : 0.0f;
-    sub = lanes_sum<LT>(g * z);
-    d = g * z;
+    r = lanes_sum<LT>(g * z);
   }
   if (lane < p.k) part[tl][lane] = int2{idx, __float_as_int(d)};
   wave_lds_fence();
-  // dx_e = (what the choices of expert e give) - score * sub
+  // what the choices of each expert give
   float dx[NE];
 #pragma unroll
-  for (int i = 0; i < NE; ++i) dx[i] = -(x[i] * sub);
+  for (int i = 0; i < NE; ++i) dx[i] = 0.0f;
   for (int j = 0; j < p.k; ++j) {
     const int2 c = part[tl][j];
     const int at = c.x - e0;
 #pragma unroll
     for (int i = 0; i < NE; ++i) dx[i] += at == i ? __int_as_float(c.y) : 0.0f;
+  }
+  if (p.softmax && !p.renorm) {  // score * (its gradient less their mean), in two steps as above
+    float left = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NE; ++i) {
+      dx[i] -= r;
+      left += dx[i] * x[i];
+    }
+    left = lanes_sum<LT>(left);
+#pragma unroll
+    for (int i = 0; i < NE; ++i) dx[i] = x[i] * (dx[i] - left);
   }
   const int64_t out = (int64_t)t * p.so + e0;
   if (p.out_bf16) {

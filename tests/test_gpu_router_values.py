@@ -76,3 +76,69 @@ def test_gradient_of_confident_sigmoid_experts(T, E, k, bf16):
     np.put_along_axis(ref, idx.astype(np.int64), 1.5 * g.astype(np.float64) / (1 + np.exp(-z)) / (1 + np.exp(z)), 1)
     err = np.abs(out.cpu().numpy() - ref)
     assert np.all(err <= 12 * U * np.abs(ref)), f"largest relative error {np.max(err / np.maximum(np.abs(ref), 1e-300))}"
+
+
+@pytest.mark.parametrize("score,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True)])
+@pytest.mark.parametrize("T,E,k", [(300, 64, 6), (100, 256, 8), (40, 33, 1), (50, 60, 20)])
+def test_gradient_of_confident_rows(score, renorm, T, E, k):
+    """Weights that are a mean's: the gradient of one is
+        q_j sum_i q_i (g_j - g_i),
+    which is small where one expert has nearly all of the weight, though the
+    g_i are not.  Its terms carry the relative error e = (k + 40 + 4 max|x -
+    max|) u of their weights, and the mean that is taken off is off by e of the
+    largest |g|, once more by e: |error| <= q_j (4 e sum_i q_i |g_j - g_i| +
+    4 e^2 max|g|).  (sigmoid, renormalised: q = s / D, times 1 - s_j, and 1e-20
+    g_j / D beside the sum; for softmax weights as they are, the sum is over all
+    experts, those not chosen with g = 0.)"""
+    say(f"moe_route_topk_bwd confident rows T={T} E={E} k={k} {score} renorm={renorm}")
+    rng = np.random.default_rng(80 + E + k)
+    x = rng.normal(size=(T, E)).astype(np.float32)
+    idx = np.argsort(rng.uniform(size=(T, E)), axis=1)[:, :k].astype(np.int32)
+    rows = np.arange(T)
+    if score == "softmax":
+        x[rows, idx[:, 0]] += rng.uniform(0, 30, size=T).astype(np.float32)  # one chosen expert stands out
+    else:
+        x[:, :] -= rng.uniform(0, 60, size=(T, 1)).astype(np.float32)
+        x[rows, idx[:, 0]] += rng.uniform(0, 40, size=T).astype(np.float32)
+    if k > 2:
+        idx[5, 2] = -1
+        idx[6, 1] = idx[6, 0]          # named twice
+    g = (rng.normal(size=(T, k)) + 2.0).astype(np.float32)
+    d, xv = _logits(x, False, pad=1)
+    out = torch.empty(T, E, device="cuda")
+    _mg().moe_route_topk_bwd(d, to_dev(idx), to_dev(g), out, score=score, renormalize=renorm, scale=1.0)
+    got = out.cpu().numpy().astype(np.float64)
+    ok = idx >= 0
+    at = np.clip(idx, 0, E - 1).astype(np.int64)
+    g64 = np.where(ok, g, 0.0).astype(np.float64)
+    spread = (xv.max(axis=1, keepdims=True) - xv.min(axis=1, keepdims=True)) if score == "softmax" else np.zeros((T, 1))
+    e = (k + 40 + 4 * spread) * U
+    gmax = np.abs(g64).max(axis=1, keepdims=True)
+    ref, bound = np.zeros((T, E)), np.full((T, E), 1e-37)
+    if score == "softmax" and not renorm:
+        p = router._scores(xv, score)
+        ds = np.zeros((T, E))
+        for j in range(k):
+            ds[rows, at[:, j]] += g64[:, j]
+        diff = ds[:, :, None] - ds[:, None, :]
+        ref = p * (p[:, None, :] * diff).sum(axis=2)
+        bound += p * (4 * e * (p[:, None, :] * np.abs(diff)).sum(axis=2) + 4 * e * e * gmax)
+    else:
+        z = np.take_along_axis(xv, at, 1)
+        if score == "softmax":
+            q = np.where(ok, np.exp(z - np.where(ok, z, -np.inf).max(axis=1, keepdims=True)), 0.0)
+            q /= q.sum(axis=1, keepdims=True)
+            rest, slope = np.zeros((T, 1)), 1.0
+        else:
+            s = np.where(ok, 1 / (1 + np.exp(-z)), 0.0)
+            D = s.sum(axis=1, keepdims=True) + 1e-20
+            q, rest, slope = s / D, 1e-20 / D, 1 / (1 + np.exp(z))
+        diff = g64[:, :, None] - g64[:, None, :]
+        r = q * slope * ((q[:, None, :] * diff).sum(axis=2) + rest * g64)
+        b = q * slope * (4 * e * ((q[:, None, :] * np.abs(diff)).sum(axis=2) + rest * np.abs(g64)) + 4 * e * e * gmax)
+        for j in range(k):
+            ref[rows, at[:, j]] += np.where(ok[:, j], r[:, j], 0.0)
+            bound[rows, at[:, j]] += np.where(ok[:, j], b[:, j], 0.0)
+    assert np.allclose(ref, router.moe_route_topk_bwd(xv, idx, g, score, renorm, 1.0), rtol=1e-6, atol=1e-12)
+    err = np.abs(got - ref)
+    assert np.all(err <= bound), f"{np.sum(err > bound)} outside, largest error / bound {np.max(err / bound)}"
