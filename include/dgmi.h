@@ -407,8 +407,9 @@ enum {
  *   renormalize  weights are divided by their sum (sigmoid: s_j / (sum +
  *                1e-20); softmax: the softmax over the chosen logits)
  *   scale        factor of every weight
- * Equal choices go to the lowest index.  An expert whose logit or bias is
- * -inf cannot be chosen (a token whose logits are all -inf is routed
+ * Without a bias the choices are ordered by the logits themselves, with one
+ * by the FP32 sums of score and bias; equal ones go to the lowest index.  An
+ * expert whose logit or bias is -inf cannot be chosen (a token whose logits are all -inf is routed
  * nowhere); NaN ranks below every number.  A +inf softmax logit makes the
  * row's weights NaN, and so does a NaN one (with renormalisation: a NaN among
  * the chosen).  Scores are FP32, each operation rounded once.

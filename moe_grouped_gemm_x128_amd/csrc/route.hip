@@ -4,12 +4,14 @@
 //
 //   scores      s = 1 / (1 + exp(-x))               (sigmoid)
 //               s = exp(x - max x) / sum            (softmax)
-//   choice      c = s + bias; softmax without bias: c = exp(x - max x), the
-//               same order without the sum's rounding
+//   choice      c = s + bias; without a bias the logit itself: scores rise with
+//               it, and in FP32 neighbours, scores near 1 and scores that
+//               underflow would become equal
 //   eligible    an expert whose logit and bias are not -inf
 //   groups      the E experts are n_group equal ranges; a group's score is
-//               the sum of its group_top (1 or 2) best eligible choices; the
-//               topk_group best groups stay
+//               its best eligible choice, or the sum of its two best s + bias
+//               (softmax without a bias: of exp(x - max x)); the topk_group
+//               best groups stay
 //   selection   the k best eligible choices of the groups that stay; ties go
 //               to the lowest index, NaN ranks below every number; -1 where
 //               fewer than k are eligible
@@ -178,40 +180,41 @@ __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_route_topk_kernel(const
   int n = p.group_size - first;
   n = n < 0 || g >= p.n_group || !live ? 0 : n > NE ? NE : n;
   const int e0 = g * p.group_size + first;
-  float x[NE], s[NE];
+  float x[NE], b[NE];
   load_run<NE>(p.logits, p.bf16, (int64_t)t * p.sl + e0, n, p.vec, -INFINITY, x);
+  if (p.bias != nullptr) load_run<NE>(p.bias, false, e0, n, p.vec_bias, 0.0f, b);
   float top = -INFINITY;  // softmax: the row's largest logit, 0 where there is none
   if (p.softmax) {
 #pragma unroll
     for (int i = 0; i < NE; ++i) top = fmaxf(top, x[i]);
     top = lanes_max<LT>(top);
     if (top == -INFINITY) top = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NE; ++i) s[i] = expf(x[i] - top);
-  } else {
-#pragma unroll
-    for (int i = 0; i < NE; ++i) s[i] = sigmoid_f32(x[i]);
   }
-  // softmax without renormalisation, or with a bias on the scores: the sum
-  float sum = 1.0f;
-  if (p.softmax && (!p.renorm || p.bias != nullptr)) {
-    sum = 0.0f;
-#pragma unroll
-    for (int i = 0; i < NE; ++i) sum += s[i];
-    sum = lanes_sum<LT>(sum);
-  }
+  // a logit's score; softmax: before the division by the sum
+  const auto score_of = [&](float v) { return p.softmax ? expf(v - top) : sigmoid_f32(v); };
   uint32_t key[NE];
-  if (p.bias != nullptr) {
-    float b[NE];
-    load_run<NE>(p.bias, false, e0, n, p.vec_bias, 0.0f, b);
+  float sum = 1.0f;  // softmax: the row's sum, where it is wanted
+  if (p.bias != nullptr || (p.softmax && !p.renorm)) {
+    float s[NE];
 #pragma unroll
-    for (int i = 0; i < NE; ++i) {
-      const float c = (p.softmax ? __fdiv_rn(s[i], sum) : s[i]) + b[i];
-      key[i] = x[i] != -INFINITY && b[i] != -INFINITY ? choice_key(c) : 0u;
+    for (int i = 0; i < NE; ++i) s[i] = score_of(x[i]);
+    if (p.softmax) {
+      sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NE; ++i) sum += s[i];
+      sum = lanes_sum<LT>(sum);
     }
-  } else {
+    if (p.bias != nullptr) {
 #pragma unroll
-    for (int i = 0; i < NE; ++i) key[i] = x[i] != -INFINITY ? choice_key(s[i]) : 0u;
+      for (int i = 0; i < NE; ++i) {
+        const float c = (p.softmax ? __fdiv_rn(s[i], sum) : s[i]) + b[i];
+        key[i] = x[i] != -INFINITY && b[i] != -INFINITY ? choice_key(c) : 0u;
+      }
+    }
+  }
+  if (p.bias == nullptr) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) key[i] = x[i] != -INFINITY ? choice_key(x[i]) : 0u;
   }
   if (p.n_group > 1) {
     // the group's two best choices, in all of its lanes
@@ -233,7 +236,12 @@ __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_route_topk_kernel(const
     if constexpr (LT >= 64)
       if (p.log_l >= 5) merge(other<16>(m1), other<16>(m2));
     uint32_t score = m1;
-    if (p.group_top == 2 && m2 != 0) score = choice_key(key_choice(m1) + key_choice(m2));
+    if (p.group_top == 2 && m1 != 0) {
+      // (without a bias the keys are those of logits)
+      const float c1 = p.bias != nullptr ? key_choice(m1) : score_of(key_choice(m1));
+      const float c2 = m2 == 0 ? 0.0f : p.bias != nullptr ? key_choice(m2) : score_of(key_choice(m2));
+      score = choice_key(c1 + c2);
+    }
     // the group stays if fewer than topk_group others are better
     int better = 0;
     const int row = (threadIdx.x & 63) - lane;  // first lane of the token
@@ -283,7 +291,7 @@ __global__ __launch_bounds__(64 * ROUTER_WAVES) void moe_route_topk_kernel(const
   if (got) {
     const int64_t at = (int64_t)t * p.sl + idx;
     xz = p.bf16 ? bf16_to_f32(static_cast<const uint16_t*>(p.logits)[at]) : static_cast<const float*>(p.logits)[at];
-    z = p.softmax ? expf(xz - top) : sigmoid_f32(xz);
+    z = score_of(xz);
   }
   float wgt;
   if (!p.softmax) {

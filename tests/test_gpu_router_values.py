@@ -142,3 +142,32 @@ def test_gradient_of_confident_rows(score, renorm, T, E, k):
     assert np.allclose(ref, router.moe_route_topk_bwd(xv, idx, g, score, renorm, 1.0), rtol=1e-6, atol=1e-12)
     err = np.abs(got - ref)
     assert np.all(err <= bound), f"{np.sum(err > bound)} outside, largest error / bound {np.max(err / bound)}"
+
+
+@pytest.mark.parametrize("T", [37, 2100, 8200])  # 64, 32 and 16 lanes a token
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups", [(128, (1, 1, 1)), (96, (8, 3, 1)), (33, (1, 1, 1))])
+def test_choice_without_a_bias_follows_the_logits(T, score, E, groups):
+    """Scores rise with their logits: without a bias the best choices are the
+    largest logits, also where FP32 scores are equal -- 0 or 1, or a logit's
+    last bits apart.  Equal logits go by index."""
+    say(f"moe_route_topk order of the logits T={T} E={E} {score} groups={groups}")
+    rng = np.random.default_rng(E + T)
+    k = 6
+    x = rng.normal(size=(T, E)).astype(np.float32)
+    x[0::6, 3] = 150.0                                         # all others underflow in a softmax
+    x[1::6] = x[1::6] * 5 + 40                                 # all sigmoids round to 1
+    x[2::6] = x[2::6] * 5 - 120                                # all sigmoids underflow
+    x[3::6] *= 1e-7                                            # close together
+    x[4::6] = np.round(x[4::6]) + 200.0                        # ties
+    d, xv = _logits(x, False, pad=2)
+    idx, w = _route(d, k, score=score, n_group=groups[0], topk_group=groups[1], group_top=1)
+    c = xv.copy()
+    if groups[0] > 1:
+        per = c.reshape(T, groups[0], -1)
+        keep = np.argsort(-per.max(axis=2), axis=1, kind="stable")[:, :groups[1]]
+        drop = np.ones((T, groups[0]), dtype=bool)
+        np.put_along_axis(drop, keep, False, axis=1)
+        per[drop] = -np.inf
+    want = np.argsort(-c, axis=1, kind="stable")[:, :k]
+    assert np.array_equal(idx.cpu().numpy(), want), f"{np.sum(np.any(idx.cpu().numpy() != want, axis=1))} rows differ"
