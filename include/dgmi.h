@@ -440,7 +440,8 @@ int moe_route_topk_bwd(const dg_tensor* logits, const dg_tensor* topk_idx, const
  *                strides that are multiples of 16 (innermost 1; tokens less
  *                than 2^24 bytes apart, pages less than 2^32): pages may be
  *                laid out head by head or token by token, and the two caches
- *                may be halves of one pool
+ *                may be parts of one pool, interleaved in any way that shares
+ *                no memory (with unlike page strides: one after the other)
  *   k_scale, v_scale  F32 [pages, Hkv], any strides (pages less than 2^30
  *                elements apart): the scale of each page and head, a power of
  *                two

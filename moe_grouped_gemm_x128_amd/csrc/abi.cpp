@@ -988,6 +988,60 @@ int check_rows_apart(const dg_tensor* t, const char* name) {
   return DG_OK;
 }
 
+// Two strided tensors whose memory ranges may interleave: is there an element
+// of both?  That is a combination of their strides, with coefficients in the
+// ranges of their indexes (b's negative, equal strides taken together), that
+// equals the distance of their bases.  Sought from the largest stride down, where
+// what the smaller ones can reach leaves one or two coefficients for tensors of
+// alike strides; a search that grows past `budget` steps counts as an overlap.
+struct Stride {
+  int64_t by, lo, hi;  // stride, range of its coefficient
+};
+bool reaches(const Stride* d, int n, int64_t left, int* budget) {
+  if (n == 0) return left == 0;
+  if (--*budget < 0) return true;
+  int64_t lo = 0, hi = 0;  // what the smaller strides reach
+  for (int i = 1; i < n; ++i) {
+    lo += d[i].lo * d[i].by;
+    hi += d[i].hi * d[i].by;
+  }
+  // the first coefficient that leaves no more than hi, up to the last that leaves no less than lo
+  const int64_t most = left - hi, least = left - lo;
+  int64_t c = most >= 0 ? (most + d->by - 1) / d->by : -(-most / d->by);
+  const int64_t end = least >= 0 ? least / d->by : -((-least + d->by - 1) / d->by);
+  if (c < d->lo) c = d->lo;
+  for (; c <= end && c <= d->hi; ++c)
+    if (reaches(d + 1, n - 1, left - c * d->by, budget)) return true;
+  return false;
+}
+int check_apart(const dg_tensor* a, const char* aname, const dg_tensor* b, const char* bname) {
+  uintptr_t a0, a1, b0, b1;
+  span(a, &a0, &a1);
+  span(b, &b0, &b1);
+  if (a0 >= a1 || b0 >= b1 || a0 >= b1 || b0 >= a1) return DG_OK;
+  Stride d[8];
+  int n = 0;
+  const auto add = [&](int64_t by, int64_t lo, int64_t hi) {
+    if (lo == hi || by == 0) return;
+    int at = 0;
+    while (at < n && d[at].by > by) ++at;
+    if (at < n && d[at].by == by) {
+      d[at].lo += lo;
+      d[at].hi += hi;
+      return;
+    }
+    for (int i = n++; i > at; --i) d[i] = d[i - 1];
+    d[at] = Stride{by, lo, hi};
+  };
+  for (int i = 0; i < a->ndim; ++i) add(a->stride[i], 0, a->shape[i] - 1);
+  for (int i = 0; i < b->ndim; ++i) add(b->stride[i], 1 - b->shape[i], 0);
+  const int64_t es = elem_size(a->dtype);  // (both bases are aligned to it)
+  int budget = 256;
+  if (reaches(d, n, ((int64_t)b0 - (int64_t)a0) / es, &budget))
+    return fail(DG_INVALID_ARG, "%s and %s overlap in memory", aname, bname);
+  return DG_OK;
+}
+
 // Logits [T, E] in FP32 or BF16.
 int check_logits(const dg_tensor* t, const char* name, const char* fname) {
   DG_TRY(check_basic(t, name, true));
@@ -1235,10 +1289,10 @@ int kv_append_fp8(const dg_tensor* k, const dg_tensor* v, const dg_tensor* k_cac
     }
     DG_TRY(check_rows_apart(outs[i], onames[i]));
   }
-  // k_cache and v_cache (and their scales) may be the two halves of one pool,
-  // page by page or head by head, but not the same memory
-  if (pages > 0 && (k_cache->data == v_cache->data || k_scale->data == v_scale->data))
-    return fail(DG_INVALID_ARG, "%s: v_cache and v_scale must not be k_cache and k_scale", fname);
+  // k_cache and v_cache (and their scales) may be parts of one pool, page by
+  // page, head by head or token by token, but share no memory
+  DG_TRY(check_apart(k_cache, "k_cache", v_cache, "v_cache"));
+  DG_TRY(check_apart(k_scale, "k_scale", v_scale, "v_scale"));
   if (T == 0 || S == 0 || pages == 0 || Hkv == 0) {
     if (q == nullptr || T == 0 || S == 0 || Hq == 0) return ok();
   }
