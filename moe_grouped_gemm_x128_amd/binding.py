@@ -87,6 +87,7 @@ class DgmiError(RuntimeError):
 
 
 _LIB = None
+_CALLS = None
 
 
 def load_library(path=None):
@@ -94,12 +95,26 @@ def load_library(path=None):
     global _LIB
     if _LIB is not None and path is None:
         return _LIB
-    p = path or LIB_PATH
+    lib = _open(path or LIB_PATH, ctypes.POINTER(DgTensor))
+    if path is None:
+        _LIB = lib
+    return lib
+
+
+def _calls():
+    """The library for this module's own calls, whose descriptors are packed bytes."""
+    global _CALLS
+    if _CALLS is None:
+        _CALLS = _open(LIB_PATH, ctypes.c_void_p)
+    return _CALLS
+
+
+def _open(p, T):
+    """The library at p, its const dg_tensor* arguments of ctypes type T."""
     if not os.path.exists(p):
         raise RuntimeError(f"libdgmi.so not found at {p}: build it with `python -m moe_grouped_gemm_x128_amd.build`")
     lib = ctypes.CDLL(p)
     vp, i64, i32, f32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_float
-    T = vp  # const dg_tensor*: packed bytes or a reference to a DgTensor
     sig = {
         "dg_last_error": ([], ctypes.c_char_p),
         "dgmi_init": ([], ctypes.c_int),
@@ -134,8 +149,6 @@ def load_library(path=None):
         fn = getattr(lib, name)
         fn.argtypes = args
         fn.restype = res
-    if path is None:
-        _LIB = lib
     return lib
 
 
@@ -214,27 +227,27 @@ def _stream(stream):
 
 def _check(rc):
     if rc != DG_OK:
-        raise DgmiError(rc, load_library().dg_last_error().decode())
+        raise DgmiError(rc, _calls().dg_last_error().decode())
 
 
 def last_error():
-    return load_library().dg_last_error().decode()
+    return _calls().dg_last_error().decode()
 
 
 def dgmi_init():
-    _check(load_library().dgmi_init())
+    _check(_calls().dgmi_init())
 
 
 def fp8_gemm_nt(a, b, sfa, sfb, c, d, stream=None):
     """d = c + a . b^T with block scales; c is None or a BF16/F32 [M, N] tensor (may be d)."""
-    lib = load_library()
+    lib = _calls()
     _check(lib.fp8_gemm_nt(_arg(a), _arg(b), _arg(sfa), _arg(sfb),
                            _arg(c), _arg(d), _stream(stream)))
     return d
 
 
 def _fp8_gemm_layout(name, a, b, sfa, sfb, c, d, stream):
-    lib = load_library()
+    lib = _calls()
     _check(getattr(lib, name)(_arg(a), _arg(b), _arg(sfa), _arg(sfb),
                               _arg(c), _arg(d), _stream(stream)))
     return d
@@ -257,7 +270,7 @@ def fp8_gemm_tt(a, b, sfa, sfb, c, d, stream=None):
 
 def fp8_gemm_nt_fp8_out(a, b, sfa, sfb, c, q, sfq, use_ue8m0=False, stream=None):
     """(q, sfq) = per-token FP8 cast of the BF16 D = c + a . b^T, in one kernel."""
-    lib = load_library()
+    lib = _calls()
     _check(lib.fp8_gemm_nt_fp8_out(_arg(a), _arg(b), _arg(sfa), _arg(sfb),
                                    _arg(c), _arg(q), _arg(sfq), int(bool(use_ue8m0)),
                                    _stream(stream)))
@@ -267,7 +280,7 @@ def fp8_gemm_nt_fp8_out(a, b, sfa, sfb, c, q, sfq, use_ue8m0=False, stream=None)
 def m_grouped_fp8_gemm_nt_contiguous(a, b, sfa, sfb, d, grouped_layout, stream=None, c=None):
     """Contiguous grouped GEMM; with c (BF16/F32, d's shape, may be d) the
     accumulate form d = c + a . b^T (m_grouped_fp8_gemm_nt_contiguous_acc)."""
-    lib = load_library()
+    lib = _calls()
     if c is not None:
         _check(lib.m_grouped_fp8_gemm_nt_contiguous_acc(_arg(a), _arg(b), _arg(sfa),
                                                         _arg(sfb), _arg(c), _arg(d),
@@ -282,7 +295,7 @@ def m_grouped_fp8_gemm_nt_contiguous(a, b, sfa, sfb, d, grouped_layout, stream=N
 def m_grouped_fp8_gemm_nt_masked(a, b, sfa, sfb, d, masked_m, max_m_per_group, stream=None, c=None):
     """Masked grouped GEMM; with c (BF16/F32, d's shape, may be d) the
     accumulate form d = c + a . b^T (m_grouped_fp8_gemm_nt_masked_acc)."""
-    lib = load_library()
+    lib = _calls()
     if c is not None:
         _check(lib.m_grouped_fp8_gemm_nt_masked_acc(_arg(a), _arg(b), _arg(sfa),
                                                     _arg(sfb), _arg(c), _arg(d),
@@ -297,7 +310,7 @@ def m_grouped_fp8_gemm_nt_masked(a, b, sfa, sfb, d, masked_m, max_m_per_group, s
 def m_grouped_bf16_gemm_nt_masked(a, b, d, masked_m, max_m_per_group, stream=None, c=None):
     """Masked grouped BF16 GEMM; with c (BF16/F32, d's shape, may be d) the
     accumulate form d = c + a . b^T (m_grouped_bf16_gemm_nt_masked_acc)."""
-    lib = load_library()
+    lib = _calls()
     if c is not None:
         _check(lib.m_grouped_bf16_gemm_nt_masked_acc(_arg(a), _arg(b), _arg(c),
                                                      _arg(d), _arg(masked_m), int(max_m_per_group),
@@ -310,7 +323,7 @@ def m_grouped_bf16_gemm_nt_masked(a, b, d, masked_m, max_m_per_group, stream=Non
 
 def bf16_gemm_nt(a, b, c, d, stream=None):
     """d = c + a . b^T in BF16 (FP32 accumulation); c is None or a BF16/F32 [M, N] tensor (may be d)."""
-    lib = load_library()
+    lib = _calls()
     _check(lib.bf16_gemm_nt(_arg(a), _arg(b), _arg(c), _arg(d),
                             _stream(stream)))
     return d
@@ -319,7 +332,7 @@ def bf16_gemm_nt(a, b, c, d, stream=None):
 def m_grouped_bf16_gemm_nt_contiguous(a, b, d, grouped_layout, stream=None, c=None):
     """Contiguous grouped BF16 GEMM; with c (BF16/F32, d's shape, may be d)
     the accumulate form d = c + a . b^T (m_grouped_bf16_gemm_nt_contiguous_acc)."""
-    lib = load_library()
+    lib = _calls()
     if c is not None:
         _check(lib.m_grouped_bf16_gemm_nt_contiguous_acc(_arg(a), _arg(b), _arg(c),
                                                          _arg(d), _arg(grouped_layout),
@@ -331,14 +344,14 @@ def m_grouped_bf16_gemm_nt_contiguous(a, b, d, grouped_layout, stream=None, c=No
 
 
 def per_token_cast_to_fp8(x, q, sf, use_ue8m0=False, stream=None):
-    lib = load_library()
+    lib = _calls()
     _check(lib.per_token_cast_to_fp8(_arg(x), _arg(q), _arg(sf),
                                      int(bool(use_ue8m0)), _stream(stream)))
     return q, sf
 
 
 def per_block_cast_to_fp8(x, q, sf, use_ue8m0=False, stream=None):
-    lib = load_library()
+    lib = _calls()
     _check(lib.per_block_cast_to_fp8(_arg(x), _arg(q), _arg(sf),
                                      int(bool(use_ue8m0)), _stream(stream)))
     return q, sf
@@ -348,7 +361,7 @@ def pack_ue8m0_to_int(x, out, invalid_count=None, stream=None):
     """Pack FP32 power-of-two scales into int32 words of four UE8M0 bytes.
     invalid_count: optional int32 device tensor (1 element) that receives the
     number of non-UE8M0 inputs, added on the device."""
-    lib = load_library()
+    lib = _calls()
     cnt = ctypes.c_void_p(invalid_count.data_ptr()) if invalid_count is not None else None
     _check(lib.pack_ue8m0_to_int(_arg(x), _arg(out), cnt, _stream(stream)))
     return out
@@ -357,7 +370,7 @@ def pack_ue8m0_to_int(x, out, invalid_count=None, stream=None):
 def moe_dispatch_masked_fp8(x, topk_idx, a, sfa, masked_m, slot, src, use_ue8m0=False, stream=None):
     """Route (token, choice) pairs into the expert buffers a / sfa (masked
     layout) with the per-token FP8 cast; fills masked_m, slot and src."""
-    lib = load_library()
+    lib = _calls()
     _check(lib.moe_dispatch_masked_fp8(_arg(x), _arg(topk_idx), _arg(a),
                                        _arg(sfa), _arg(masked_m), _arg(slot),
                                        _arg(src), int(bool(use_ue8m0)), _stream(stream)))
@@ -369,7 +382,7 @@ def moe_dispatch_contiguous_fp8(x, topk_idx, a, sfa, grouped_layout, counts, slo
     """Route (token, choice) pairs into the contiguous layout (a region of
     whole `align`-row granules per expert, align 128 or 256) with the
     per-token FP8 cast; fills grouped_layout, counts and slot."""
-    lib = load_library()
+    lib = _calls()
     _check(lib.moe_dispatch_contiguous_fp8(_arg(x), _arg(topk_idx), _arg(a),
                                            _arg(sfa), _arg(grouped_layout), _arg(counts),
                                            _arg(slot), int(align), int(bool(use_ue8m0)), _stream(stream)))
@@ -378,7 +391,7 @@ def moe_dispatch_contiguous_fp8(x, topk_idx, a, sfa, grouped_layout, counts, slo
 
 def moe_combine(d, slot, topk_weights, y, stream=None):
     """y[t] = sum_j topk_weights[t, j] * d[slot[t, j]] (BF16 out)."""
-    lib = load_library()
+    lib = _calls()
     _check(lib.moe_combine(_arg(d), _arg(slot), _arg(topk_weights), _arg(y),
                            _stream(stream)))
     return y
@@ -399,7 +412,7 @@ def moe_route_topk(logits, topk_idx, topk_weights, bias=None, score="softmax", n
     (the tables of moe_dispatch_* and moe_combine).  score "softmax" or
     "sigmoid"; bias counts for the choice only; groups: the topk_group best of
     n_group ranges of experts by the sum of their group_top best choices."""
-    lib = load_library()
+    lib = _calls()
     _check(lib.moe_route_topk(_arg(logits), _arg(bias), _arg(topk_idx),
                               _arg(topk_weights), _score_code(score), int(n_group), int(topk_group),
                               int(group_top), int(bool(renormalize)), float(scale), _stream(stream)))
@@ -409,7 +422,7 @@ def moe_route_topk(logits, topk_idx, topk_weights, bias=None, score="softmax", n
 def moe_route_topk_bwd(logits, topk_idx, grad_weights, grad_logits, score="softmax", renormalize=True, scale=1.0,
                        stream=None):
     """grad_logits from the gradient of moe_route_topk's weights (the choice taken as given)."""
-    lib = load_library()
+    lib = _calls()
     _check(lib.moe_route_topk_bwd(_arg(logits), _arg(topk_idx), _arg(grad_weights),
                                   _arg(grad_logits), _score_code(score), int(bool(renormalize)),
                                   float(scale), _stream(stream)))
@@ -421,7 +434,7 @@ def kv_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_toke
     """Append the tokens k, v [T, Hkv, D] to the paged FP8 caches
     [pages, Hkv, P, D] (scales [pages, Hkv]), keys rotated by position with
     cos_sin [positions, rot]; q [T, Hq, D] is rotated into q_out on the way."""
-    lib = load_library()
+    lib = _calls()
     _check(lib.kv_append_fp8(_arg(k), _arg(v), _arg(k_cache), _arg(v_cache),
                              _arg(k_scale), _arg(v_scale), _arg(block_table),
                              _arg(cu_tokens), _arg(start), _arg(cos_sin),
@@ -431,7 +444,7 @@ def kv_append_fp8(k, v, k_cache, v_cache, k_scale, v_scale, block_table, cu_toke
 
 def paged_attention_fp8_workspace(S, n, Hq, Hkv, D, max_tokens):
     """Bytes of workspace paged_attention_fp8 needs (max_tokens = max_pages * P)."""
-    return int(load_library().paged_attention_fp8_workspace(int(S), int(n), int(Hq), int(Hkv), int(D),
+    return int(_calls().paged_attention_fp8_workspace(int(S), int(n), int(Hq), int(Hkv), int(D),
                                                             int(max_tokens)))
 
 
@@ -439,7 +452,7 @@ def paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_
                         lse=None, window=0, stream=None):
     """Attention of the n newest tokens of each sequence, q [S, n, Hq, D],
     over its pages of the FP8 caches; lse [S, n, Hq] is optional."""
-    lib = load_library()
+    lib = _calls()
     _check(lib.paged_attention_fp8(_arg(q), _arg(k_cache), _arg(v_cache),
                                    _arg(k_scale), _arg(v_scale), _arg(block_table),
                                    _arg(seq_lens), _arg(out), _arg(lse),
@@ -449,6 +462,6 @@ def paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_
 
 def query_config(kind, G, M, N, K):
     cfg = DgConfig()
-    _check(load_library().dg_query_config(int(kind), int(G), int(M), int(N), int(K), ctypes.byref(cfg)))
+    _check(_calls().dg_query_config(int(kind), int(G), int(M), int(N), int(K), ctypes.byref(cfg)))
     return dict(block_m=cfg.block_m, block_n=cfg.block_n, threads=cfg.threads, grid=cfg.grid, lds_bytes=cfg.lds_bytes,
                 n_split=cfg.n_split, block_n2=cfg.block_n2, grid2=cfg.grid2, lds_bytes2=cfg.lds_bytes2)
