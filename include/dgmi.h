@@ -501,7 +501,8 @@ int paged_attention_fp8(const dg_tensor* q, const dg_tensor* k_cache, const dg_t
                         const dg_tensor* workspace, float scale, int32_t window, hipStream_t stream);
 
 /* Bytes of workspace that paged_attention_fp8 needs for these sizes
- * (max_tokens = max_pages * P); a pure function of its arguments. */
+ * (max_tokens = max_pages * P); a pure function of its arguments.  0 for sizes
+ * that no call takes. */
 int64_t paged_attention_fp8_workspace(int64_t S, int64_t n, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_tokens);
 
 /* Launch configuration chosen for a GEMM (a pure function of the shapes).

@@ -1351,7 +1351,10 @@ int kv_append_fp8(const dg_tensor* k, const dg_tensor* v, const dg_tensor* k_cac
 }
 
 int64_t paged_attention_fp8_workspace(int64_t S, int64_t n, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_tokens) {
-  if (S <= 0 || n <= 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || max_tokens <= 0) return 0;
+  // sizes that no call takes need none (and the plan is made for those that one takes)
+  for (int64_t v : {S, n, Hq, Hkv, max_tokens})
+    if (v <= 0 || v > INT32_MAX) return 0;
+  if ((D != 64 && D != 128 && D != 256) || Hq % Hkv != 0) return 0;
   return dgmi::paged_attention_workspace(S, n, Hq, Hkv, D, max_tokens);
 }
 
