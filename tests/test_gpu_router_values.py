@@ -10,7 +10,7 @@ import pytest
 from oracle import router
 
 from helpers import say, to_dev
-from test_gpu_router import _logits, _mg, _route
+from test_gpu_router import CHOICE_GAP, _logits, _mg, _route
 
 pytestmark = pytest.mark.gpu
 
@@ -171,3 +171,80 @@ def test_choice_without_a_bias_follows_the_logits(T, score, E, groups):
         per[drop] = -np.inf
     want = np.argsort(-c, axis=1, kind="stable")[:, :k]
     assert np.array_equal(idx.cpu().numpy(), want), f"{np.sum(np.any(idx.cpu().numpy() != want, axis=1))} rows differ"
+
+
+def _picks_by_value(x, k, idx, w, bias, kw, what):
+    """Every row of a routing against float64, near ties by value.
+
+    The picks are distinct eligible experts; position by position their float64
+    choice is the oracle's within CHOICE_GAP of the values it is made of (a near
+    tie may go either way and nothing else may); where there are groups, against
+    the best of the groups that the picks show to be kept, each of which scores
+    within the gap of the last one that the oracle keeps.  The weights are those
+    of the kernel's own picks, in every row."""
+    bias64 = None if bias is None else bias.astype(np.float64)
+    score, n_group, topk_group, top = (kw.get(n, d) for n, d in (("score", "softmax"), ("n_group", 1), ("topk_group", 1),
+                                                                ("group_top", 1)))
+    idx, w = idx.cpu().numpy(), w.cpu().numpy().astype(np.float64)
+    c = router.route_choices(x, bias64, score, 1, 1, 1)
+    size = np.abs(np.where(np.isfinite(c), c, 0.0)) + router._scores(x, score)
+    finite = np.where(np.isfinite(x), x, 0.0)
+    spread = np.abs(finite - finite.max(axis=1, keepdims=True)).max() if score == "softmax" else 0.0
+    swapped = 0
+    for t in range(len(x)):
+        got = idx[t][idx[t] >= 0]
+        assert np.all(idx[t][len(got):] == -1) and len(set(got.tolist())) == len(got), f"{what}: row {t}"
+        ct = c[t].copy()
+        if n_group > 1:
+            per = ct.reshape(n_group, -1)
+            rank = np.array([np.sort(g[g > -np.inf])[::-1][:top].sum() if np.any(g > -np.inf) else -np.inf for g in per])
+            gap = CHOICE_GAP * 2 * size[t].reshape(n_group, -1).max(axis=1)
+            cut = np.sort(rank)[::-1][topk_group - 1]
+            shown = np.unique(got // per.shape[1])
+            with np.errstate(invalid="ignore"):
+                near = np.abs(rank - cut) <= gap
+            sure = (rank > cut) & ~near
+            assert len(shown) <= topk_group and np.all((sure | near)[shown]), f"{what}: row {t}, groups"
+            # the groups that can be kept: what is sure, what the picks show, and the best near ones
+            rest = [g for g in np.argsort(-rank, kind="stable") if near[g] and g not in shown]
+            keep = set(np.flatnonzero(sure).tolist()) | set(shown.tolist())
+            keep |= set(rest[:max(0, topk_group - len(keep))])
+            per[[g for g in range(n_group) if g not in keep]] = -np.inf
+        best = np.argsort(-ct, kind="stable")[:k]
+        best = best[ct[best] > -np.inf]
+        assert len(best) == len(got), f"{what}: row {t}, {len(got)} picks of {len(best)}"
+        off = np.abs(c[t][got] - ct[best])
+        assert np.all(off <= CHOICE_GAP * np.maximum(size[t][got], size[t][best])), f"{what}: row {t}"
+        swapped += not np.array_equal(got, best)
+        rw = router.route_weights(x[t], idx[t], score, kw.get("renormalize", True), kw.get("scale", 1.0))
+        assert np.all(np.abs(w[t] - rw) <= (k + 20 + 2 * spread) * U * np.abs(rw) + 1e-37), f"{what}: row {t}, weights"
+    return swapped
+
+
+@pytest.mark.parametrize("T,E,k,score,bias,groups,renorm,step", [
+    (300, 256, 8, "sigmoid", True, (8, 4, 2), True, 0),
+    (200, 64, 6, "softmax", False, (8, 3, 1), False, 0),
+    (50, 1024, 64, "sigmoid", True, (64, 32, 2), True, 0),       # the limits: many near ties
+    (50, 513, 5, "softmax", False, (27, 13, 2), True, 0),
+    (100, 60, 4, "softmax", True, (1, 1, 1), False, 0),
+    # logits so close that most neighbours are near ties
+    (200, 128, 8, "sigmoid", True, (1, 1, 1), True, 1e-7),
+    (200, 128, 8, "sigmoid", True, (8, 3, 2), False, 2e-7),
+    (200, 128, 8, "softmax", True, (8, 3, 1), True, 2e-7),
+    (2100, 96, 6, "softmax", False, (8, 3, 2), True, 3e-7),
+    (8200, 64, 6, "sigmoid", False, (8, 3, 2), True, 3e-7),
+])
+def test_near_ties_by_value(T, E, k, score, bias, groups, renorm, step):
+    say(f"moe_route_topk near ties T={T} E={E} k={k} {score} groups={groups} step={step}")
+    rng = np.random.default_rng(500 + E + T)
+    if step:
+        x = (0.5 + rng.integers(-20, 20, size=(T, E)) * step).astype(np.float32)
+    else:
+        x = (rng.normal(size=(T, E)) * 2).astype(np.float32)
+    x[7, E // 2:], x[8] = -np.inf, -np.inf
+    b = (rng.integers(-3, 4, size=E) * max(step, 0.02)).astype(np.float32) if bias else None
+    d, xv = _logits(x, False)
+    kw = dict(score=score, n_group=groups[0], topk_group=groups[1], group_top=groups[2], renormalize=renorm, scale=1.5)
+    idx, w = _route(d, k, bias=None if b is None else to_dev(b), **kw)
+    swapped = _picks_by_value(xv, k, idx, w, b, kw, f"T={T} E={E}")
+    say(f"  {swapped} rows with a near tie the other way")
