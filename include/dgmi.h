@@ -409,10 +409,11 @@ enum {
  *   scale        factor of every weight
  * Without a bias the choices are ordered by the logits themselves, with one
  * by the FP32 sums of score and bias; equal ones go to the lowest index.  An
- * expert whose logit or bias is -inf cannot be chosen (a token whose logits are all -inf is routed
- * nowhere); NaN ranks below every number.  A +inf softmax logit makes the
- * row's weights NaN, and so does a NaN one (with renormalisation: a NaN among
- * the chosen).  Scores are FP32, each operation rounded once.
+ * expert whose logit or bias is -inf cannot be chosen (a token whose logits are
+ * all -inf is routed nowhere); NaN ranks below every number.  A +inf softmax
+ * logit makes the row's weights NaN, and so does a NaN one (with
+ * renormalisation: a NaN among the chosen).  Scores are FP32, each operation
+ * rounded once.
  */
 int moe_route_topk(const dg_tensor* logits, const dg_tensor* bias, const dg_tensor* topk_idx,
                    const dg_tensor* topk_weights, int32_t score, int32_t n_group, int32_t topk_group,
@@ -478,7 +479,8 @@ int kv_append_fp8(const dg_tensor* k, const dg_tensor* v, const dg_tensor* k_cac
  *             of 8 elements, 16-byte aligned bases
  *   caches, scales, block_table  as kv_append_fp8; Hq a multiple of Hkv (query
  *             heads h * Hq / Hkv .. share KV head h).  Scales of pages that
- *             a query sees are positive and finite
+ *             a query sees are positive, finite and not subnormal, V's within
+ *             a factor of 2^120 of each other
  *   seq_lens  I32 [S]: tokens in the cache, the n queries' own included (cut
  *             to what the block table holds).  Query i stands at position
  *             seq_lens[s] - n + i
@@ -491,9 +493,11 @@ int kv_append_fp8(const dg_tensor* k, const dg_tensor* v, const dg_tensor* k_cac
  *   window    a query sees the window positions up to its own; 0: all of them
  * Positions past a query's own or before its window, and pages outside
  * [0, pages), take no part, whatever their memory holds (NaN codes too, and
- * the scales of pages that no query sees).  A query that sees nothing gives 0, with lse -inf.  Weights are rounded to FP16
- * on their way into the second product, sums and output accumulate in FP32.
- * The result does not depend on the order in which workgroups run.
+ * the scales of pages that no query sees).  A query that sees nothing gives 0,
+ * with lse -inf.  Weights are rounded to FP16 (11 bits) on their way into the
+ * second product, scores, sums and output accumulate in FP32; a finite score
+ * gives a finite row, however large it is.  The result does not depend on the
+ * order in which workgroups run.
  */
 int paged_attention_fp8(const dg_tensor* q, const dg_tensor* k_cache, const dg_tensor* v_cache,
                         const dg_tensor* k_scale, const dg_tensor* v_scale, const dg_tensor* block_table,

@@ -21,7 +21,7 @@
 // The backward takes the choice as given: with z_j = s of choice j, D = sum
 // z_j + 1e-20 and g the gradient of the weights,
 //   dz_j = scale g_j, renormalised scale (g_j - sum_i g_i z_i / D) / D,
-//   sigmoid  dx_e = dz_e s_e (1 - s_e),
+//   sigmoid  dx_e = dz_e s_e (1 - s_e), 1 - s_e as s(-x_e),
 //   softmax  dx_e = s_e (dz_e - sum_j dz_j z_j),
 //   softmax, renormalised: with q the softmax over the chosen logits,
 //            dx_j = scale q_j (g_j - sum_i g_i q_i), and zero elsewhere.
@@ -35,10 +35,13 @@
 // has it.
 //
 // What bounds it: a token's logits are read once (16384 x 256 FP32: 3.5 us at
-// the copy rate), but the scores (an accurate exponential and a division each)
-// and the rounds are about 450 instructions of a wave per token of 256 experts:
-// 17.5 us for 16384 tokens on 1024 SIMDs.  One token takes 4.1 us, of which a
-// launch is about 2.
+// the copy rate), but the scores that a bias asks for (an accurate exponential
+// and a division each) and the rounds are about 530 vector instructions of a wave
+// per token of 256 experts: 16 us for 16384 tokens on 1024 SIMDs.  Without a bias
+// only the chosen experts' scores are formed: 160 per token of 128 experts, 7.1 us
+// for 16384 tokens, whose waves spend 54% of their cycles waiting, 20% waiting to
+// issue and 26% issuing (each round hangs on the one before it).  One token takes
+// 4.3 us, of which a launch is about 2.
 
 #include "common.hpp"
 #include "launch.hpp"
@@ -463,9 +466,10 @@ hipError_t launch_moe_route_topk(RouteTopkArgs p, hipStream_t stream) {
   };
   // Few tokens: many lanes, whose rounds are the shortest; many: few lanes, of
   // which four or two tokens share an instruction.  Measured with 64 / 32 / 16
-  // lanes, in us: 256 tokens, 256 experts (8 of them, 4 of 8 groups) 5.3 / 6.5
-  // / 10.0, 4096 tokens 7.9 / 7.4 / 8.6, 16384 tokens 20.6 / 18.7 / 17.5;
-  // 128 experts without groups 4.5 / 4.9 / 5.4, 5.7 / 5.3 / 5.3, 13.1 / 10.3 / 8.0.
+  // lanes, in us: 256 tokens, 256 experts with a bias (8 of them, 4 of 8 groups)
+  // 5.4 / 6.8 / 10.3, 4096 tokens 7.9 / 7.6 / 9.2, 16384 tokens 19.6 / 17.1 / 16.0;
+  // 128 experts without bias and groups 4.4 / 4.7 / 5.2, 5.6 / 5.0 / 5.1, 12.0 / 9.3
+  // / 7.1.
   if (!(p.T > 8192 && place(16)) && !(p.T > 2048 && place(32))) place(64);
   const int chunk = 16 / es;
   p.vec = p.group_size % chunk == 0 && ne % chunk == 0 && aligned16(p.logits, p.sl * es, p.T);
@@ -484,8 +488,8 @@ hipError_t launch_moe_route_topk(RouteTopkArgs p, hipStream_t stream) {
 hipError_t launch_moe_route_topk_bwd(RouteTopkBwdArgs p, hipStream_t stream) {
   const int es = p.bf16 ? 2 : 4, oes = p.out_bf16 ? 2 : 4;
   // At most eight experts to a lane, so that a token's lanes write whole lines:
-  // 16384 tokens with 64 / 32 / 16 lanes took 8.4 / 7.4 / 10.2 us for 256
-  // experts, 7.3 / 5.2 / 4.6 us for 128, 6.6 / 4.9 / 4.0 us for 64.
+  // 16384 tokens with 64 / 32 / 16 lanes took 9.7 / 8.1 / 10.0 us for 256
+  // experts, 7.6 / 6.1 / 5.6 us for 128, 6.9 / 5.3 / 4.5 us for 64.
   const int lt = p.k <= 16 && p.E <= 128 ? 16 : p.k <= 32 && p.E <= 256 ? 32 : 64;
   const int ne = pow2_up((p.E + lt - 1) / lt);
   p.vec = p.E % (16 / es) == 0 && ne % (16 / es) == 0 && aligned16(p.logits, p.sl * es, p.T);
