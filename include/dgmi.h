@@ -495,9 +495,10 @@ int kv_append_fp8(const dg_tensor* k, const dg_tensor* v, const dg_tensor* k_cac
  * [0, pages), take no part, whatever their memory holds (NaN codes too, and
  * the scales of pages that no query sees).  A query that sees nothing gives 0,
  * with lse -inf.  Weights are rounded to FP16 (11 bits) on their way into the
- * second product, scores, sums and output accumulate in FP32; a finite score
- * gives a finite row, however large it is.  The result does not depend on the
- * order in which workgroups run.
+ * second product -- those below 2^-38 of the row's largest, V's scales counted
+ * in, are lost there -- while scores, sums and output accumulate in FP32; a
+ * finite score gives a finite row, however large it is.  The result does not
+ * depend on the order in which workgroups run.
  */
 int paged_attention_fp8(const dg_tensor* q, const dg_tensor* k_cache, const dg_tensor* v_cache,
                         const dg_tensor* k_scale, const dg_tensor* v_scale, const dg_tensor* block_table,

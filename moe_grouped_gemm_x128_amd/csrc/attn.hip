@@ -29,9 +29,9 @@
 // the scale of V is taken into the exponent: with y_t = x_t log2 e + log2 sv_t,
 //   o = sum_t 2^(y_t - M) code_t / sum_t 2^(y_t - M) / sv_t,  M = max y,
 // and P is held times 2^14, so that weights down to 2^-28 of the largest are
-// normal numbers.  (An FP32 P would be exact and cost the matrix cores' rate for
-// FP16; against 64 bits the BF16 output is off by 1.658e-3 of itself, with FP32
-// weights by 1.654e-3.)
+// normal numbers and those below 2^-39 vanish.  (More bits would cost the matrix
+// cores' rate for FP16; against 64 bits the BF16 output is off by 1.658e-3 of
+// itself, with FP32 weights by 1.654e-3.)
 // Sums, maxima and the output stay in FP32.
 //
 // Work is cut along the cache by device-side lengths: the 32-token tiles of
