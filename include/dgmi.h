@@ -11,7 +11,9 @@
  *    for SM90 and SM100", section 2 (NT layout, FP32 or packed UE8M0 scale
  *    factors) and section 4 (fp8_gemm_nt(a, b, a_sf, b_sf, c, bf16)).
  * Around them: casts, the MoE steps (choice of experts, dispatch, combine),
- * and a paged FP8 key/value cache with the attention over it.
+ * a paged FP8 key/value cache with the attention over it, and what a layer is
+ * trained with: norm and activation with their gradients, BF16 products of
+ * ragged groups.
  *
  * Conventions shared by every entry point
  *   - Every buffer is device memory allocated and owned by the caller,
@@ -509,6 +511,109 @@ int paged_attention_fp8(const dg_tensor* q, const dg_tensor* k_cache, const dg_t
  * (max_tokens = max_pages * P); a pure function of its arguments.  0 for sizes
  * that no call takes. */
 int64_t paged_attention_fp8_workspace(int64_t S, int64_t n, int64_t Hq, int64_t Hkv, int64_t D, int64_t max_tokens);
+
+/*
+ * Root-mean-square norm with the residual's addition, and its result cast to
+ * FP8 in the same kernel (the operand of the FP8 GEMMs):
+ *   h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight
+ *   x         F32 or BF16 [T, H], or [T, heads, H] (each head of a projection's
+ *             output), any strides of the outer dims (innermost 1); H <= 16384
+ *   weight    F32 or BF16 [H]
+ *   residual  NULL, or F32 or BF16 of x's shape
+ *   h         NULL, or of the residual's type and x's shape, out: the sum,
+ *             rounded once.  The norm is of the rounded sum, stored or not
+ *   y         NULL, or F32 or BF16 of x's shape, out
+ *   q, sf     both NULL, or E4M3 of x's shape and F32 [.., ceil(H/128)] (any
+ *             strides), out: y, unrounded, cast as per_token_cast_to_fp8 casts
+ *             (one scale per 128 elements of a row, amax floored at 1e-4; with
+ *             use_ue8m0 rounded up to a power of two).  Values that are not
+ *             finite become NaN codes and do not count for the scale
+ *   eps       positive and finite
+ * One of y and q is wanted.  h and y may take the place of x or the residual
+ * (same base, type and strides); any other overlap is rejected.  Rows whose
+ * squares leave FP32's range are computed as those of smaller ones.
+ */
+int rms_norm(const dg_tensor* x, const dg_tensor* weight, const dg_tensor* y, const dg_tensor* q, const dg_tensor* sf,
+             const dg_tensor* residual, const dg_tensor* h, float eps, int use_ue8m0, hipStream_t stream);
+
+/*
+ * Gradients of rms_norm's y with respect to the sum h (so to x and to the
+ * residual alike) and to the weight; a cast of y counts as the identity.
+ *   grad_y       F32 or BF16 [T, H] or [T, heads, H]
+ *   h            the sum that rms_norm stored (x, where it had no residual)
+ *   grad_x       F32 or BF16 of that shape, out; it may take the place of
+ *                grad_y, h or grad_h (same base, type and strides)
+ *   grad_weight  NULL, or F32 or BF16 [H], out
+ *   workspace    F32, rms_norm_bwd_workspace(rows, H) bytes (rows = T heads), 16-byte
+ *                aligned; NULL without grad_weight.  Its contents mean nothing
+ *                between calls, but two calls that may run at once need one each
+ *   grad_h       NULL, or F32 or BF16 of that shape: a gradient that reaches h
+ *                from elsewhere (the residual stream), added to grad_x
+ * FP32 sums in an order that depends on the sizes only.
+ */
+int rms_norm_bwd(const dg_tensor* grad_y, const dg_tensor* h, const dg_tensor* weight, const dg_tensor* grad_x,
+                 const dg_tensor* grad_weight, const dg_tensor* workspace, const dg_tensor* grad_h, float eps,
+                 hipStream_t stream);
+
+/* Bytes of workspace that rms_norm_bwd needs for a weight's gradient; a pure
+ * function of its arguments.  0 for sizes that no call takes. */
+int64_t rms_norm_bwd_workspace(int64_t rows, int64_t H);
+
+/*
+ * The gated activation between an expert's two products, with its cast to FP8:
+ *   y = row_weight * silu(gate) * up,  silu(g) = g / (1 + exp(-g))
+ *   x            F32 or BF16 [R, 2 I] or [G, R, 2 I]: the gate's I columns, then
+ *                the up projection's
+ *   y            NULL, or F32 or BF16 [.., I], out
+ *   q, sf        both NULL, or E4M3 [.., I] and F32 [.., ceil(I/128)], out: y,
+ *                unrounded, cast as by rms_norm
+ *   masked_m     NULL, or I32 [G] ([1] for a 2-D x) on the device: only the
+ *                first masked_m[g] rows of group g are read and written (the
+ *                masked GEMM's layout; with a 2-D x the rows in use of a buffer)
+ *   row_weights  NULL, or F32 [G R]: a factor of each row (the router's weights)
+ */
+int swiglu(const dg_tensor* x, const dg_tensor* y, const dg_tensor* q, const dg_tensor* sf, const dg_tensor* masked_m,
+           const dg_tensor* row_weights, int use_ue8m0, hipStream_t stream);
+
+/*
+ * Gradients of swiglu's y; a cast of y counts as the identity.
+ *   grad_y            F32 or BF16 [.., I]
+ *   grad_x            F32 or BF16 of x's shape, out; it may be x itself
+ *   grad_row_weights  NULL, or F32 [G R], out: the sum over each row of grad_y
+ *                     silu(gate) up (for moe_route_topk_bwd)
+ * masked_m and row_weights as for swiglu; rows past masked_m are left alone.
+ */
+int swiglu_bwd(const dg_tensor* x, const dg_tensor* grad_y, const dg_tensor* grad_x, const dg_tensor* masked_m,
+               const dg_tensor* row_weights, const dg_tensor* grad_row_weights, hipStream_t stream);
+
+/*
+ * BF16 products grouped by expert with ragged sizes: rows sorted by expert, no
+ * padding between the groups.  Group g holds rows offsets[g] .. offsets[g+1]-1
+ * of the tokens' tensors (device memory, never read by the host; values are cut
+ * to [0, M], a group whose end is not past its start is empty).  offsets is
+ * expected not to fall: where it does, which rows of d are computed is not
+ * specified.  FP32 accumulation.
+ *   nt  d[m] = c[m] + a[m] . b[g]^T   a [M, K], b [G, N, K], d [M, N]: the
+ *       forward product of m_grouped_bf16_gemm_nt_contiguous without its blocks
+ *   nn  d[m] = c[m] + a[m] . b[g]     a [M, K], b [G, K, N], d [M, N]: the
+ *       gradient of nt's a, from nt's b as it is stored
+ *   tn  d[g] = c[g] + a_g^T . b_g     a [M, N], b [M, K], d [G, N, K]: the
+ *       gradient of nt's b, the contraction over the group's rows; an empty
+ *       group gives c[g], or zeros
+ *   a, b     BF16, row and group strides multiples of 8 elements, 16-byte
+ *            aligned bases; any M, N and (tn) K, K of nt and nn a multiple of 64
+ *   c        NULL, or BF16 or F32 of d's shape; it may be d itself (same base,
+ *            type and strides), any other overlap is rejected
+ *   d        BF16 or F32, any row stride (innermost 1).  Rows of nt and nn
+ *            outside every group are neither read from a and c nor written
+ *   offsets  I32 [G + 1]
+ */
+int m_grouped_bf16_gemm_nt_ragged(const dg_tensor* a, const dg_tensor* b, const dg_tensor* c, const dg_tensor* d,
+                                  const dg_tensor* offsets, hipStream_t stream);
+int m_grouped_bf16_gemm_nn_ragged(const dg_tensor* a, const dg_tensor* b, const dg_tensor* c, const dg_tensor* d,
+                                  const dg_tensor* offsets, hipStream_t stream);
+int k_grouped_bf16_gemm_tn(const dg_tensor* a, const dg_tensor* b, const dg_tensor* c, const dg_tensor* d,
+                           const dg_tensor* offsets, hipStream_t stream);
 
 /* Launch configuration chosen for a GEMM (a pure function of the shapes).
  * A GEMM is one launch over all N columns, or two launches in stream order:

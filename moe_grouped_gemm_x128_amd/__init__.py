@@ -33,5 +33,13 @@ from .binding import (  # noqa: F401
     kv_append_fp8,
     paged_attention_fp8,
     paged_attention_fp8_workspace,
+    rms_norm,
+    rms_norm_bwd,
+    rms_norm_bwd_workspace,
+    swiglu,
+    swiglu_bwd,
+    m_grouped_bf16_gemm_nt_ragged,
+    m_grouped_bf16_gemm_nn_ragged,
+    k_grouped_bf16_gemm_tn,
     query_config,
 )

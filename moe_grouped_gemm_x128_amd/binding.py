@@ -52,6 +52,14 @@ ENTRY_POINTS = (
     "kv_append_fp8",
     "paged_attention_fp8",
     "paged_attention_fp8_workspace",
+    "rms_norm",
+    "rms_norm_bwd",
+    "rms_norm_bwd_workspace",
+    "swiglu",
+    "swiglu_bwd",
+    "m_grouped_bf16_gemm_nt_ragged",
+    "m_grouped_bf16_gemm_nn_ragged",
+    "k_grouped_bf16_gemm_tn",
     "dg_query_config",
 )
 
@@ -143,6 +151,14 @@ def _open(p, T):
         "kv_append_fp8": ([T] * 12 + [ctypes.c_int, vp], ctypes.c_int),
         "paged_attention_fp8": ([T] * 10 + [f32, i32, vp], ctypes.c_int),
         "paged_attention_fp8_workspace": ([i64] * 6, i64),
+        "rms_norm": ([T] * 7 + [f32, ctypes.c_int, vp], ctypes.c_int),
+        "rms_norm_bwd": ([T] * 7 + [f32, vp], ctypes.c_int),
+        "rms_norm_bwd_workspace": ([i64] * 2, i64),
+        "swiglu": ([T] * 6 + [ctypes.c_int, vp], ctypes.c_int),
+        "swiglu_bwd": ([T] * 6 + [vp], ctypes.c_int),
+        "m_grouped_bf16_gemm_nt_ragged": ([T] * 5 + [vp], ctypes.c_int),
+        "m_grouped_bf16_gemm_nn_ragged": ([T] * 5 + [vp], ctypes.c_int),
+        "k_grouped_bf16_gemm_tn": ([T] * 5 + [vp], ctypes.c_int),
         "dg_query_config": ([i32, i64, i64, i64, i64, ctypes.POINTER(DgConfig)], ctypes.c_int),
     }
     for name, (args, res) in sig.items():
@@ -458,6 +474,67 @@ def paged_attention_fp8(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_
                                    _arg(seq_lens), _arg(out), _arg(lse),
                                    _arg(workspace), float(scale), int(window), _stream(stream)))
     return out
+
+
+def rms_norm(x, weight, y=None, q=None, sf=None, residual=None, h=None, eps=1e-6, use_ue8m0=False, stream=None):
+    """Norm of the rows of x [T, H] or [T, heads, H], or of x + residual (stored
+    in h): y, and / or its FP8 cast q with the scales sf [.., ceil(H / 128)]."""
+    lib = _calls()
+    _check(lib.rms_norm(_arg(x), _arg(weight), _arg(y), _arg(q), _arg(sf), _arg(residual),
+                        _arg(h), float(eps), int(bool(use_ue8m0)), _stream(stream)))
+    return y if q is None else (q, sf)
+
+
+def rms_norm_bwd_workspace(rows, H):
+    """Bytes of workspace rms_norm_bwd needs for the gradient of the weight (rows = T * heads)."""
+    return int(_calls().rms_norm_bwd_workspace(int(rows), int(H)))
+
+
+def rms_norm_bwd(grad_y, h, weight, grad_x, grad_weight=None, workspace=None, grad_h=None, eps=1e-6, stream=None):
+    """grad_x (of x and of the residual alike; grad_h, what reaches the sum from
+    elsewhere, is added) and grad_weight from the gradient of rms_norm's y."""
+    lib = _calls()
+    _check(lib.rms_norm_bwd(_arg(grad_y), _arg(h), _arg(weight), _arg(grad_x), _arg(grad_weight),
+                            _arg(workspace), _arg(grad_h), float(eps), _stream(stream)))
+    return grad_x
+
+
+def swiglu(x, y=None, q=None, sf=None, masked_m=None, row_weights=None, use_ue8m0=False, stream=None):
+    """row_weights * silu(gate) * up of x [.., 2 I] (the gate's columns first): y,
+    and / or its FP8 cast q, sf; of the first masked_m[g] rows of each group only."""
+    lib = _calls()
+    _check(lib.swiglu(_arg(x), _arg(y), _arg(q), _arg(sf), _arg(masked_m), _arg(row_weights),
+                      int(bool(use_ue8m0)), _stream(stream)))
+    return y if q is None else (q, sf)
+
+
+def swiglu_bwd(x, grad_y, grad_x, masked_m=None, row_weights=None, grad_row_weights=None, stream=None):
+    """grad_x (it may be x) and grad_row_weights from the gradient of swiglu's y."""
+    lib = _calls()
+    _check(lib.swiglu_bwd(_arg(x), _arg(grad_y), _arg(grad_x), _arg(masked_m), _arg(row_weights),
+                          _arg(grad_row_weights), _stream(stream)))
+    return grad_x
+
+
+def m_grouped_bf16_gemm_nt_ragged(a, b, d, offsets, stream=None, c=None):
+    """d[m] = c[m] + a[m] . b[g]^T for rows offsets[g] <= m < offsets[g + 1]."""
+    lib = _calls()
+    _check(lib.m_grouped_bf16_gemm_nt_ragged(_arg(a), _arg(b), _arg(c), _arg(d), _arg(offsets), _stream(stream)))
+    return d
+
+
+def m_grouped_bf16_gemm_nn_ragged(a, b, d, offsets, stream=None, c=None):
+    """d[m] = c[m] + a[m] . b[g] for rows offsets[g] <= m < offsets[g + 1], b [G, K, N]."""
+    lib = _calls()
+    _check(lib.m_grouped_bf16_gemm_nn_ragged(_arg(a), _arg(b), _arg(c), _arg(d), _arg(offsets), _stream(stream)))
+    return d
+
+
+def k_grouped_bf16_gemm_tn(a, b, d, offsets, stream=None, c=None):
+    """d[g] = c[g] + a_g^T . b_g over rows offsets[g] .. offsets[g + 1] - 1 of a [M, N] and b [M, K]."""
+    lib = _calls()
+    _check(lib.k_grouped_bf16_gemm_tn(_arg(a), _arg(b), _arg(c), _arg(d), _arg(offsets), _stream(stream)))
+    return d
 
 
 def query_config(kind, G, M, N, K):

@@ -23,7 +23,8 @@ LIB = os.path.join(HERE, "libdgmi.so")
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"
 
-SOURCES = ["abi.cpp", "quant.hip", "gemm.hip", "moe.hip", "route.hip", "kvcache.hip", "attn.hip"]
+SOURCES = ["abi.cpp", "quant.hip", "gemm.hip", "moe.hip", "route.hip", "kvcache.hip", "attn.hip", "norm.hip",
+           "swiglu.hip", "ragged.hip"]
 
 COMMON_FLAGS = [
     f"--offload-arch={ARCH}",

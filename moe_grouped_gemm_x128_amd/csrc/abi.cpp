@@ -1464,6 +1464,510 @@ int paged_attention_fp8(const dg_tensor* q, const dg_tensor* k_cache, const dg_t
   return check_launch(dgmi::launch_paged_attention(p, stream), fname);
 }
 
+namespace {
+
+// Rows of a norm: [T, H], or [T, heads, H] with any strides of the first two.
+struct Rows {
+  int64_t n0, n1, H, s0, s1;
+};
+int check_norm_rows(const dg_tensor* t, const char* name, const Rows* like, Rows* v, const char* fname) {
+  DG_TRY(check_basic(t, name, true));
+  if (t->ndim != 2 && t->ndim != 3) return fail(DG_INVALID_ARG, "%s: %s must be [T, H] or [T, heads, H]", fname, name);
+  v->n0 = t->shape[0];
+  v->n1 = t->ndim == 3 ? t->shape[1] : 1;
+  v->H = t->shape[t->ndim - 1];
+  v->s0 = t->stride[0];
+  v->s1 = t->ndim == 3 ? t->stride[1] : 0;
+  if (like != nullptr && (v->n0 != like->n0 || v->n1 != like->n1 || v->H != like->H))
+    return fail(DG_INVALID_ARG, "%s: %s must have the shape of %s", fname, name, "the input");
+  if (!aligned(t->data, elem_size(t->dtype))) return fail(DG_INVALID_ARG, "%s: %s must be element-aligned", fname, name);
+  return DG_OK;
+}
+int check_f32_bf16(const dg_tensor* t, const char* name, const char* fname) {
+  if (t->dtype != DG_F32 && t->dtype != DG_BF16) return fail(DG_INVALID_ARG, "%s: %s must be F32 or BF16", fname, name);
+  return DG_OK;
+}
+// Do all rows start on `bytes`?
+bool rows_on(const dg_tensor* t, int bytes) {
+  for (int i = 0; i < t->ndim; ++i)
+    if (t->shape[i] == 0) return true;
+  bool on = aligned(t->data, bytes);
+  for (int i = 0; i + 1 < t->ndim; ++i) on = on && (t->shape[i] <= 1 || t->stride[i] * elem_size(t->dtype) % bytes == 0);
+  return on;
+}
+bool same_memory(const dg_tensor* a, const dg_tensor* b) {
+  if (a->data != b->data || a->dtype != b->dtype || a->ndim != b->ndim) return false;
+  for (int i = 0; i < a->ndim; ++i)
+    if (a->shape[i] != b->shape[i] || (a->shape[i] > 1 && a->stride[i] != b->stride[i])) return false;
+  return true;
+}
+// FP8 output [.., n] and its block scales [.., ceil(n / 128)], of the leading shape of x.
+int check_fp8_out(const dg_tensor* q, const dg_tensor* sf, const dg_tensor* x, int64_t n, const char* fname) {
+  if ((q == nullptr) != (sf == nullptr)) return fail(DG_INVALID_ARG, "%s: q and sf go together", fname);
+  if (q == nullptr) return DG_OK;
+  DG_TRY(check_basic(q, "q", true));
+  DG_TRY(check_dtype(q, "q", DG_E4M3));
+  DG_TRY(check_basic(sf, "sf", false));
+  DG_TRY(check_dtype(sf, "sf", DG_F32));
+  if (!aligned(sf->data, 4)) return fail(DG_INVALID_ARG, "%s: sf must be 4-byte aligned", fname);
+  bool ok = q->ndim == x->ndim && sf->ndim == x->ndim && q->shape[q->ndim - 1] == n &&
+            sf->shape[sf->ndim - 1] == (n + 127) / 128;
+  for (int i = 0; ok && i + 1 < x->ndim; ++i) ok = q->shape[i] == x->shape[i] && sf->shape[i] == x->shape[i];
+  if (!ok)
+    return fail(DG_INVALID_ARG, "%s: q must be [.., %lld] and sf [.., %lld], of the input's rows", fname, (long long)n,
+                (long long)((n + 127) / 128));
+  DG_TRY(check_rows_apart(q, "q"));
+  DG_TRY(check_rows_apart(sf, "sf"));
+  return DG_OK;
+}
+constexpr int64_t kMaxNormRow = 16384;
+// Workgroups of up to 1024 threads.
+constexpr int64_t kMaxGroups1024 = (int64_t(1) << 22) - 1;
+
+}  // namespace
+
+int rms_norm(const dg_tensor* x, const dg_tensor* weight, const dg_tensor* y, const dg_tensor* q, const dg_tensor* sf,
+             const dg_tensor* residual, const dg_tensor* h, float eps, int use_ue8m0, hipStream_t stream) {
+  const char* fname = "rms_norm";
+  Rows vx, vr = {}, vh = {}, vy = {};
+  DG_TRY(check_norm_rows(x, "x", nullptr, &vx, fname));
+  DG_TRY(check_f32_bf16(x, "x", fname));
+  const int64_t H = vx.H, rows = vx.n0 * vx.n1;
+  DG_TRY(check_basic(weight, "weight", true));
+  DG_TRY(check_f32_bf16(weight, "weight", fname));
+  if (weight->ndim != 1 || weight->shape[0] != H) return fail(DG_INVALID_ARG, "%s: weight must be [H = %lld]", fname, (long long)H);
+  if (!aligned(weight->data, elem_size(weight->dtype))) return fail(DG_INVALID_ARG, "%s: weight must be element-aligned", fname);
+  if (residual != nullptr) {
+    DG_TRY(check_norm_rows(residual, "residual", &vx, &vr, fname));
+    DG_TRY(check_f32_bf16(residual, "residual", fname));
+  }
+  if (h != nullptr) {
+    if (residual == nullptr) return fail(DG_INVALID_ARG, "%s: h is the sum of x and residual: it needs a residual", fname);
+    DG_TRY(check_norm_rows(h, "h", &vx, &vh, fname));
+    DG_TRY(check_dtype(h, "h", residual->dtype));
+    DG_TRY(check_rows_apart(h, "h"));
+  }
+  if (y == nullptr && q == nullptr) return fail(DG_INVALID_ARG, "%s: one of y and q is wanted", fname);
+  if (y != nullptr) {
+    DG_TRY(check_norm_rows(y, "y", &vx, &vy, fname));
+    DG_TRY(check_f32_bf16(y, "y", fname));
+    DG_TRY(check_rows_apart(y, "y"));
+  }
+  DG_TRY(check_fp8_out(q, sf, x, H, fname));
+  if (!(eps > 0.0f && eps - eps == 0.0f)) return fail(DG_INVALID_ARG, "%s: eps must be positive and finite", fname);
+  if (H > kMaxNormRow) return fail(DG_UNSUPPORTED, "%s: rows of at most %lld elements (got %lld)", fname, (long long)kMaxNormRow, (long long)H);
+  if (rows > kMaxGroups1024) return fail(DG_UNSUPPORTED, "%s: at most 2^22 - 1 rows a call (got %lld)", fname, (long long)rows);
+  const dg_tensor* outs[] = {h, y, q, sf};
+  const char* onames[] = {"h", "y", "q", "sf"};
+  const dg_tensor* ins[] = {x, residual, weight};
+  const char* inames[] = {"x", "residual", "weight"};
+  for (int i = 0; i < 4; ++i) {
+    if (outs[i] == nullptr) continue;
+    for (int j = 0; j < 3; ++j) {
+      // a row is read whole before it is written: h and y may take the place of x or residual
+      if (i < 2 && j < 2 && ins[j] != nullptr && same_memory(outs[i], ins[j])) continue;
+      DG_TRY(check_no_alias(outs[i], onames[i], ins[j], inames[j]));
+    }
+    for (int j = i + 1; j < 4; ++j) DG_TRY(check_no_alias(outs[i], onames[i], outs[j], onames[j]));
+  }
+  if (rows == 0 || H == 0) return ok();
+  dgmi::RmsNormArgs p = {};
+  p.x = x->data;
+  p.x_bf16 = x->dtype == DG_BF16;
+  p.x_vec = rows_on(x, 16);
+  p.sx_0 = vx.s0;
+  p.sx_1 = vx.s1;
+  p.w = weight->data;
+  p.w_bf16 = weight->dtype == DG_BF16;
+  p.w_vec = aligned(weight->data, 16);
+  if (residual != nullptr) {
+    p.res = residual->data;
+    p.r_bf16 = residual->dtype == DG_BF16;
+    p.r_vec = rows_on(residual, 16);
+    p.sr_0 = vr.s0;
+    p.sr_1 = vr.s1;
+  }
+  if (h != nullptr) {
+    p.h = h->data;
+    p.h_vec = rows_on(h, 16);
+    p.sh_0 = vh.s0;
+    p.sh_1 = vh.s1;
+  }
+  if (y != nullptr) {
+    p.y = y->data;
+    p.y_bf16 = y->dtype == DG_BF16;
+    p.y_vec = rows_on(y, 16);
+    p.sy_0 = vy.s0;
+    p.sy_1 = vy.s1;
+  }
+  if (q != nullptr) {
+    p.q = static_cast<uint8_t*>(q->data);
+    p.q_vec = rows_on(q, 8);
+    p.sq_0 = q->stride[0];
+    p.sq_1 = q->ndim == 3 ? q->stride[1] : 0;
+    p.sf = static_cast<float*>(sf->data);
+    p.ss_0 = sf->stride[0];
+    p.ss_1 = sf->ndim == 3 ? sf->stride[1] : 0;
+    p.ss_k = sf->stride[sf->ndim - 1];
+  }
+  p.rows = rows;
+  p.heads = vx.n1;
+  p.H = (int32_t)H;
+  p.ue8m0 = use_ue8m0 ? 1 : 0;
+  p.eps = eps;
+  return check_launch(dgmi::launch_rms_norm(p, stream), fname);
+}
+
+int64_t rms_norm_bwd_workspace(int64_t rows, int64_t H) {
+  if (rows <= 0 || rows > kMaxGroups1024 || H <= 0 || H > kMaxNormRow) return 0;
+  return dgmi::rms_norm_bwd_parts(rows, H) * H * 4;
+}
+
+int rms_norm_bwd(const dg_tensor* grad_y, const dg_tensor* h, const dg_tensor* weight, const dg_tensor* grad_x,
+                 const dg_tensor* grad_weight, const dg_tensor* workspace, const dg_tensor* grad_h, float eps,
+                 hipStream_t stream) {
+  const char* fname = "rms_norm_bwd";
+  Rows vh, vg, vx, vd = {};
+  DG_TRY(check_norm_rows(h, "h", nullptr, &vh, fname));
+  DG_TRY(check_norm_rows(grad_y, "grad_y", &vh, &vg, fname));
+  DG_TRY(check_norm_rows(grad_x, "grad_x", &vh, &vx, fname));
+  for (const dg_tensor* t : {h, grad_y, grad_x}) DG_TRY(check_f32_bf16(t, t == h ? "h" : t == grad_y ? "grad_y" : "grad_x", fname));
+  const int64_t H = vh.H, rows = vh.n0 * vh.n1;
+  if (grad_h != nullptr) {
+    DG_TRY(check_norm_rows(grad_h, "grad_h", &vh, &vd, fname));
+    DG_TRY(check_f32_bf16(grad_h, "grad_h", fname));
+  }
+  for (const dg_tensor* t : {weight, grad_weight}) {
+    const char* name = t == weight ? "weight" : "grad_weight";
+    if (t == nullptr && t == grad_weight) continue;
+    DG_TRY(check_basic(t, name, true));
+    DG_TRY(check_f32_bf16(t, name, fname));
+    if (t->ndim != 1 || t->shape[0] != H) return fail(DG_INVALID_ARG, "%s: %s must be [H = %lld]", fname, name, (long long)H);
+    if (!aligned(t->data, elem_size(t->dtype))) return fail(DG_INVALID_ARG, "%s: %s must be element-aligned", fname, name);
+  }
+  if (!(eps > 0.0f && eps - eps == 0.0f)) return fail(DG_INVALID_ARG, "%s: eps must be positive and finite", fname);
+  if (H > kMaxNormRow) return fail(DG_UNSUPPORTED, "%s: rows of at most %lld elements (got %lld)", fname, (long long)kMaxNormRow, (long long)H);
+  if (rows > kMaxGroups1024) return fail(DG_UNSUPPORTED, "%s: at most 2^22 - 1 rows a call (got %lld)", fname, (long long)rows);
+  DG_TRY(check_rows_apart(grad_x, "grad_x"));
+  const int64_t need = grad_weight != nullptr ? rms_norm_bwd_workspace(rows, H) : 0;
+  if (need > 0) {
+    if (workspace == nullptr) return fail(DG_INVALID_ARG, "%s: workspace of %lld bytes needed", fname, (long long)need);
+    DG_TRY(check_basic(workspace, "workspace", true));
+    DG_TRY(check_dtype(workspace, "workspace", DG_F32));
+    if (workspace->ndim != 1 || workspace->shape[0] * 4 < need)
+      return fail(DG_INVALID_ARG, "%s: workspace must be F32 [at least %lld]", fname, (long long)(need / 4));
+    if (!aligned(workspace->data, 16)) return fail(DG_INVALID_ARG, "%s: workspace must be 16-byte aligned", fname);
+  }
+  const dg_tensor* outs[] = {grad_x, grad_weight, need > 0 ? workspace : nullptr};
+  const char* onames[] = {"grad_x", "grad_weight", "workspace"};
+  const dg_tensor* ins[] = {grad_y, h, grad_h, weight};
+  const char* inames[] = {"grad_y", "h", "grad_h", "weight"};
+  for (int i = 0; i < 3; ++i) {
+    if (outs[i] == nullptr) continue;
+    for (int j = 0; j < 4; ++j) {
+      // a row is read whole before it is written: grad_x may take the place of one of its inputs
+      if (i == 0 && j < 3 && ins[j] != nullptr && same_memory(outs[i], ins[j])) continue;
+      DG_TRY(check_no_alias(outs[i], onames[i], ins[j], inames[j]));
+    }
+    for (int j = i + 1; j < 3; ++j) DG_TRY(check_no_alias(outs[i], onames[i], outs[j], onames[j]));
+  }
+  if (H == 0) return ok();
+  dgmi::RmsNormBwdArgs p = {};
+  p.dy = grad_y->data;
+  p.dy_bf16 = grad_y->dtype == DG_BF16;
+  p.dy_vec = rows_on(grad_y, 16);
+  p.sg_0 = vg.s0;
+  p.sg_1 = vg.s1;
+  p.h = h->data;
+  p.h_bf16 = h->dtype == DG_BF16;
+  p.h_vec = rows_on(h, 16);
+  p.sh_0 = vh.s0;
+  p.sh_1 = vh.s1;
+  p.w = weight->data;
+  p.w_bf16 = weight->dtype == DG_BF16;
+  p.w_vec = aligned(weight->data, 16);
+  if (grad_h != nullptr) {
+    p.dh = grad_h->data;
+    p.dh_bf16 = grad_h->dtype == DG_BF16;
+    p.dh_vec = rows_on(grad_h, 16);
+    p.sd_0 = vd.s0;
+    p.sd_1 = vd.s1;
+  }
+  p.dx = grad_x->data;
+  p.dx_bf16 = grad_x->dtype == DG_BF16;
+  p.dx_vec = rows_on(grad_x, 16);
+  p.sx_0 = vx.s0;
+  p.sx_1 = vx.s1;
+  if (grad_weight != nullptr) {
+    p.dw = grad_weight->data;
+    p.dw_bf16 = grad_weight->dtype == DG_BF16;
+    p.part = need > 0 ? static_cast<float*>(workspace->data) : nullptr;
+  }
+  p.rows = rows;
+  p.heads = vh.n1;
+  p.H = (int32_t)H;
+  p.eps = eps;
+  return check_launch(dgmi::launch_rms_norm_bwd(p, stream), fname);
+}
+
+namespace {
+
+// The activation's input [R, 2I] or [G, R, 2I], what it makes or is given [.., I],
+// and the rows that count.
+struct Gated {
+  int64_t G, R, I;
+};
+int check_gated(const dg_tensor* x, const char* name, Gated* v, const char* fname) {
+  DG_TRY(check_basic(x, name, true));
+  DG_TRY(check_f32_bf16(x, name, fname));
+  if ((x->ndim != 2 && x->ndim != 3) || x->shape[x->ndim - 1] % 2 != 0)
+    return fail(DG_INVALID_ARG, "%s: %s must be [R, 2 I] or [G, R, 2 I]", fname, name);
+  if (!aligned(x->data, elem_size(x->dtype))) return fail(DG_INVALID_ARG, "%s: %s must be element-aligned", fname, name);
+  v->G = x->ndim == 3 ? x->shape[0] : 1;
+  v->R = x->shape[x->ndim - 2];
+  v->I = x->shape[x->ndim - 1] / 2;
+  return DG_OK;
+}
+int check_half(const dg_tensor* y, const char* name, const dg_tensor* x, int64_t I, const char* fname) {
+  DG_TRY(check_basic(y, name, true));
+  DG_TRY(check_f32_bf16(y, name, fname));
+  bool ok = y->ndim == x->ndim && y->shape[y->ndim - 1] == I;
+  for (int i = 0; ok && i + 1 < x->ndim; ++i) ok = y->shape[i] == x->shape[i];
+  if (!ok) return fail(DG_INVALID_ARG, "%s: %s must be [.., I = %lld], of x's rows", fname, name, (long long)I);
+  if (!aligned(y->data, elem_size(y->dtype))) return fail(DG_INVALID_ARG, "%s: %s must be element-aligned", fname, name);
+  return DG_OK;
+}
+int check_gated_rows(const dg_tensor* masked_m, const dg_tensor* row_weights, const Gated& v, const char* wname,
+                     const char* fname) {
+  if (masked_m != nullptr) DG_TRY(check_ints(masked_m, "masked_m", v.G, fname));
+  if (row_weights != nullptr) {
+    DG_TRY(check_basic(row_weights, wname, false));
+    DG_TRY(check_dtype(row_weights, wname, DG_F32));
+    if (row_weights->ndim != 1 || row_weights->shape[0] != v.G * v.R)
+      return fail(DG_INVALID_ARG, "%s: %s must be F32 [rows of x = %lld]", fname, wname, (long long)(v.G * v.R));
+    if (!aligned(row_weights->data, 4)) return fail(DG_INVALID_ARG, "%s: %s must be 4-byte aligned", fname, wname);
+  }
+  return DG_OK;
+}
+int64_t group_stride(const dg_tensor* t) { return t->ndim == 3 ? t->stride[0] : 0; }
+int64_t row_stride(const dg_tensor* t) { return t->stride[t->ndim - 2]; }
+// Does the second half of each row start on 16 bytes too?
+bool half_on(const dg_tensor* t, int64_t I) { return rows_on(t, 16) && I * elem_size(t->dtype) % 16 == 0; }
+
+}  // namespace
+
+int swiglu(const dg_tensor* x, const dg_tensor* y, const dg_tensor* q, const dg_tensor* sf, const dg_tensor* masked_m,
+           const dg_tensor* row_weights, int use_ue8m0, hipStream_t stream) {
+  const char* fname = "swiglu";
+  Gated v;
+  DG_TRY(check_gated(x, "x", &v, fname));
+  if (y == nullptr && q == nullptr) return fail(DG_INVALID_ARG, "%s: one of y and q is wanted", fname);
+  if (y != nullptr) {
+    DG_TRY(check_half(y, "y", x, v.I, fname));
+    DG_TRY(check_rows_apart(y, "y"));
+  }
+  DG_TRY(check_fp8_out(q, sf, x, v.I, fname));
+  DG_TRY(check_gated_rows(masked_m, row_weights, v, "row_weights", fname));
+  if (v.G * v.R > INT32_MAX || dgmi::swiglu_grid(v.G * v.R, v.I) > kMaxGroups)
+    return fail(DG_UNSUPPORTED, "%s: too many rows for one launch", fname);
+  const dg_tensor* outs[] = {y, q, sf};
+  const char* onames[] = {"y", "q", "sf"};
+  const dg_tensor* ins[] = {x, masked_m, row_weights};
+  const char* inames[] = {"x", "masked_m", "row_weights"};
+  for (int i = 0; i < 3; ++i) {
+    if (outs[i] == nullptr) continue;
+    for (int j = 0; j < 3; ++j) DG_TRY(check_no_alias(outs[i], onames[i], ins[j], inames[j]));
+    for (int j = i + 1; j < 3; ++j) DG_TRY(check_no_alias(outs[i], onames[i], outs[j], onames[j]));
+  }
+  if (v.G * v.R == 0 || v.I == 0) return ok();
+  dgmi::SwigluArgs p = {};
+  p.x = x->data;
+  p.x_bf16 = x->dtype == DG_BF16;
+  p.x_vec = rows_on(x, 16);
+  p.u_vec = half_on(x, v.I);
+  p.sx_g = group_stride(x);
+  p.sx_r = row_stride(x);
+  p.masked = masked_m ? static_cast<const int32_t*>(masked_m->data) : nullptr;
+  if (row_weights != nullptr) {
+    p.w = static_cast<const float*>(row_weights->data);
+    p.sw = row_weights->stride[0];
+  }
+  if (y != nullptr) {
+    p.y = y->data;
+    p.y_bf16 = y->dtype == DG_BF16;
+    p.y_vec = rows_on(y, 16);
+    p.sy_g = group_stride(y);
+    p.sy_r = row_stride(y);
+  }
+  if (q != nullptr) {
+    p.q = static_cast<uint8_t*>(q->data);
+    p.q_vec = rows_on(q, 8);
+    p.sq_g = group_stride(q);
+    p.sq_r = row_stride(q);
+    p.sf = static_cast<float*>(sf->data);
+    p.ss_g = group_stride(sf);
+    p.ss_r = row_stride(sf);
+    p.ss_k = sf->stride[sf->ndim - 1];
+  }
+  p.G = (int32_t)v.G;
+  p.R = (int32_t)v.R;
+  p.I = (int32_t)v.I;
+  p.ue8m0 = use_ue8m0 ? 1 : 0;
+  return check_launch(dgmi::launch_swiglu(p, stream), fname);
+}
+
+int swiglu_bwd(const dg_tensor* x, const dg_tensor* grad_y, const dg_tensor* grad_x, const dg_tensor* masked_m,
+               const dg_tensor* row_weights, const dg_tensor* grad_row_weights, hipStream_t stream) {
+  const char* fname = "swiglu_bwd";
+  Gated v, vd;
+  DG_TRY(check_gated(x, "x", &v, fname));
+  DG_TRY(check_gated(grad_x, "grad_x", &vd, fname));
+  if (grad_x->ndim != x->ndim || vd.G != v.G || vd.R != v.R || vd.I != v.I)
+    return fail(DG_INVALID_ARG, "%s: grad_x must have the shape of x", fname);
+  DG_TRY(check_rows_apart(grad_x, "grad_x"));
+  DG_TRY(check_half(grad_y, "grad_y", x, v.I, fname));
+  DG_TRY(check_gated_rows(masked_m, row_weights, v, "row_weights", fname));
+  DG_TRY(check_gated_rows(nullptr, grad_row_weights, v, "grad_row_weights", fname));
+  if (grad_row_weights != nullptr) DG_TRY(check_rows_apart(grad_row_weights, "grad_row_weights"));
+  if (v.G * v.R > INT32_MAX || dgmi::swiglu_bwd_grid(v.G * v.R, v.I) > kMaxGroups)
+    return fail(DG_UNSUPPORTED, "%s: too many rows for one launch", fname);
+  const dg_tensor* outs[] = {grad_x, grad_row_weights};
+  const char* onames[] = {"grad_x", "grad_row_weights"};
+  const dg_tensor* ins[] = {x, grad_y, masked_m, row_weights};
+  const char* inames[] = {"x", "grad_y", "masked_m", "row_weights"};
+  for (int i = 0; i < 2; ++i) {
+    if (outs[i] == nullptr) continue;
+    for (int j = 0; j < 4; ++j) {
+      // an element's inputs are read by the lane that writes its gradients: in place over x
+      if (i == 0 && j == 0 && same_memory(outs[i], ins[j])) continue;
+      DG_TRY(check_no_alias(outs[i], onames[i], ins[j], inames[j]));
+    }
+    for (int j = i + 1; j < 2; ++j) DG_TRY(check_no_alias(outs[i], onames[i], outs[j], onames[j]));
+  }
+  if (v.G * v.R == 0 || v.I == 0) {
+    if (v.G * v.R == 0 || grad_row_weights == nullptr) return ok();
+  }
+  dgmi::SwigluBwdArgs p = {};
+  p.x = x->data;
+  p.x_bf16 = x->dtype == DG_BF16;
+  p.x_vec = rows_on(x, 16);
+  p.u_vec = half_on(x, v.I);
+  p.sx_g = group_stride(x);
+  p.sx_r = row_stride(x);
+  p.dy = grad_y->data;
+  p.dy_bf16 = grad_y->dtype == DG_BF16;
+  p.dy_vec = rows_on(grad_y, 16);
+  p.sy_g = group_stride(grad_y);
+  p.sy_r = row_stride(grad_y);
+  p.masked = masked_m ? static_cast<const int32_t*>(masked_m->data) : nullptr;
+  if (row_weights != nullptr) {
+    p.w = static_cast<const float*>(row_weights->data);
+    p.sw = row_weights->stride[0];
+  }
+  p.dx = grad_x->data;
+  p.dx_bf16 = grad_x->dtype == DG_BF16;
+  p.dx_vec = rows_on(grad_x, 16);
+  p.du_vec = half_on(grad_x, v.I);
+  p.sd_g = group_stride(grad_x);
+  p.sd_r = row_stride(grad_x);
+  if (grad_row_weights != nullptr) {
+    p.dw = static_cast<float*>(grad_row_weights->data);
+    p.sdw = grad_row_weights->stride[0];
+  }
+  p.G = (int32_t)v.G;
+  p.R = (int32_t)v.R;
+  p.I = (int32_t)v.I;
+  return check_launch(dgmi::launch_swiglu_bwd(p, stream), fname);
+}
+
+namespace {
+
+// The ragged products.  nt: a [M, K], b [G, N, K], d [M, N]; nn: a [M, K], b [G, K, N],
+// d [M, N]; tn: a [M, N], b [M, K], d [G, N, K].
+int ragged_common(int layout, const dg_tensor* a, const dg_tensor* b, const dg_tensor* c, const dg_tensor* d,
+                  const dg_tensor* offsets, hipStream_t stream, const char* fname) {
+  const bool tn = layout == dgmi::RAGGED_TN;
+  DG_TRY(check_basic(a, "a", true));
+  DG_TRY(check_basic(b, "b", true));
+  DG_TRY(check_basic(d, "d", true));
+  DG_TRY(check_dtype(a, "a", DG_BF16));
+  DG_TRY(check_dtype(b, "b", DG_BF16));
+  DG_TRY(check_f32_bf16(d, "d", fname));
+  if (a->ndim != 2 || b->ndim != (tn ? 2 : 3) || d->ndim != (tn ? 3 : 2))
+    return fail(DG_INVALID_ARG, tn ? "%s: a and b must be [M, ..], d [G, N, K]" : "%s: a and d must be 2-D, b 3-D", fname);
+  DG_TRY(check_basic(offsets, "offsets", true));
+  if (offsets->ndim != 1 || offsets->shape[0] < 1) return fail(DG_INVALID_ARG, "%s: offsets must be I32 [G + 1]", fname);
+  const int64_t G = tn ? d->shape[0] : b->shape[0], M = a->shape[0];
+  DG_TRY(check_ints(offsets, "offsets", G + 1, fname));
+  const int64_t N = layout == dgmi::RAGGED_NT ? b->shape[1] : tn ? a->shape[1] : b->shape[2];
+  const int64_t K = tn ? b->shape[1] : a->shape[1];
+  if (tn ? b->shape[0] != M : b->shape[layout == dgmi::RAGGED_NT ? 2 : 1] != K)
+    return fail(DG_INVALID_ARG, "%s: a is [%lld, %lld], b [.., %lld, %lld]: they do not go together", fname, (long long)M,
+                (long long)a->shape[1], (long long)b->shape[b->ndim - 2], (long long)b->shape[b->ndim - 1]);
+  const int64_t d0 = tn ? N : M, d1 = tn ? K : N;
+  if (d->shape[d->ndim - 2] != d0 || d->shape[d->ndim - 1] != d1)
+    return fail(DG_INVALID_ARG, "%s: d must be [.., %lld, %lld]", fname, (long long)d0, (long long)d1);
+  if (!tn && K % 64 != 0) return fail(DG_UNSUPPORTED, "%s: K = %lld is not a multiple of 64", fname, (long long)K);
+  for (const dg_tensor* t : {a, b})
+    if (!rows_on(t, 16)) return fail(DG_INVALID_ARG, "%s: a and b need 16-byte aligned bases and row/group strides", fname);
+  DG_TRY(check_row_strides(2 * row_stride(a), 2 * row_stride(b), fname));
+  if (!aligned(d->data, elem_size(d->dtype))) return fail(DG_INVALID_ARG, "%s: d must be element-aligned", fname);
+  DG_TRY(check_rows_apart(d, "d"));
+  if (c != nullptr) {
+    DG_TRY(check_basic(c, "c", true));
+    DG_TRY(check_f32_bf16(c, "c", fname));
+    bool ok = c->ndim == d->ndim;
+    for (int i = 0; ok && i < d->ndim; ++i) ok = c->shape[i] == d->shape[i];
+    if (!ok) return fail(DG_INVALID_ARG, "%s: c must have the shape of d", fname);
+    if (!aligned(c->data, elem_size(c->dtype))) return fail(DG_INVALID_ARG, "%s: c must be element-aligned", fname);
+    if (!same_memory(c, d)) DG_TRY(check_no_alias(d, "d", c, "c"));
+  }
+  DG_TRY(check_no_alias(d, "d", a, "a"));
+  DG_TRY(check_no_alias(d, "d", b, "b"));
+  DG_TRY(check_no_alias(d, "d", offsets, "offsets"));
+  if (G == 0 || N == 0 || (tn ? K : M) == 0) return ok();
+  if (dgmi::ragged_grid(layout, G, M, N, K) > (INT32_MAX >> 9)) return fail(DG_UNSUPPORTED, "%s: too many tiles for one launch", fname);
+  dgmi::RaggedArgs p = {};
+  p.a = static_cast<const uint16_t*>(a->data);
+  p.b = static_cast<const uint16_t*>(b->data);
+  p.d = d->data;
+  p.c = c != nullptr ? c->data : nullptr;
+  p.offsets = static_cast<const int32_t*>(offsets->data);
+  p.lda = a->stride[0];
+  p.ldb = row_stride(b);
+  p.b_gs = group_stride(b);
+  p.ldd = row_stride(d);
+  p.d_gs = group_stride(d);
+  p.d_f32 = d->dtype == DG_F32;
+  if (c != nullptr) {
+    p.ldc = row_stride(c);
+    p.c_gs = group_stride(c);
+    p.c_f32 = c->dtype == DG_F32;
+  }
+  p.G = (int32_t)G;
+  p.M = (int32_t)M;
+  p.N = (int32_t)N;
+  p.K = (int32_t)K;
+  return check_launch(dgmi::launch_ragged(p, layout, stream), fname);
+}
+
+}  // namespace
+
+int m_grouped_bf16_gemm_nt_ragged(const dg_tensor* a, const dg_tensor* b, const dg_tensor* c, const dg_tensor* d,
+                                  const dg_tensor* offsets, hipStream_t stream) {
+  return ragged_common(dgmi::RAGGED_NT, a, b, c, d, offsets, stream, "m_grouped_bf16_gemm_nt_ragged");
+}
+
+int m_grouped_bf16_gemm_nn_ragged(const dg_tensor* a, const dg_tensor* b, const dg_tensor* c, const dg_tensor* d,
+                                  const dg_tensor* offsets, hipStream_t stream) {
+  return ragged_common(dgmi::RAGGED_NN, a, b, c, d, offsets, stream, "m_grouped_bf16_gemm_nn_ragged");
+}
+
+int k_grouped_bf16_gemm_tn(const dg_tensor* a, const dg_tensor* b, const dg_tensor* c, const dg_tensor* d,
+                           const dg_tensor* offsets, hipStream_t stream) {
+  return ragged_common(dgmi::RAGGED_TN, a, b, c, d, offsets, stream, "k_grouped_bf16_gemm_tn");
+}
+
 int dg_query_config(int32_t kind, int64_t G, int64_t M, int64_t N, int64_t K, dg_config* out) {
   if (out == nullptr) return fail(DG_INVALID_ARG, "dg_query_config: out is NULL");
   if (G < 0 || M < 0 || N < 0 || K < 0) return fail(DG_INVALID_ARG, "dg_query_config: negative size");

@@ -174,6 +174,78 @@ struct PagedAttnArgs {
   bool whole;
 };
 
+// Root-mean-square norm (norm.hip) of `rows` rows, row i at index (i / heads,
+// i % heads) of each tensor; strides in elements, *_vec: rows start on 16 bytes
+// (q: on 8).
+struct RmsNormArgs {
+  const void *x, *res, *w;
+  void *h, *y;
+  uint8_t* q;
+  float* sf;
+  int64_t sx_0, sx_1, sr_0, sr_1, sh_0, sh_1, sy_0, sy_1, sq_0, sq_1, ss_0, ss_1, ss_k;
+  int64_t rows, heads;
+  int32_t H;
+  int32_t x_bf16, r_bf16, w_bf16, y_bf16;  // h has the residual's type
+  int32_t x_vec, r_vec, w_vec, h_vec, y_vec, q_vec;
+  int32_t ue8m0;
+  float eps;
+};
+
+struct RmsNormBwdArgs {
+  const void *dy, *h, *w, *dh;
+  void* dx;
+  void* dw;     // or NULL
+  float* part;  // rms_norm_bwd_parts rows of H, NULL without dw
+  int64_t sg_0, sg_1, sh_0, sh_1, sd_0, sd_1, sx_0, sx_1;
+  int64_t rows, heads;
+  int32_t H;
+  int32_t dy_bf16, h_bf16, w_bf16, dh_bf16, dx_bf16, dw_bf16;
+  int32_t dy_vec, h_vec, w_vec, dh_vec, dx_vec;
+  float eps;
+};
+
+// Gated activation (swiglu.hip): x [G, R, 2I], y, q and dy [G, R, I]; masked [G]
+// or NULL, w [G R] or NULL.
+struct SwigluArgs {
+  const void* x;
+  const int32_t* masked;
+  const float* w;
+  void* y;
+  uint8_t* q;
+  float* sf;
+  int64_t sx_g, sx_r, sy_g, sy_r, sq_g, sq_r, ss_g, ss_r, ss_k, sw;
+  int32_t G, R, I;
+  int32_t x_bf16, y_bf16, x_vec, u_vec, y_vec, q_vec, ue8m0;
+  int32_t blocks;  // set by the launcher: 128-element blocks of a row
+};
+
+struct SwigluBwdArgs {
+  const void *x, *dy;
+  const int32_t* masked;
+  const float* w;
+  void* dx;
+  float* dw;
+  int64_t sx_g, sx_r, sy_g, sy_r, sd_g, sd_r, sw, sdw;
+  int32_t G, R, I;
+  int32_t x_bf16, dy_bf16, dx_bf16, x_vec, u_vec, dy_vec, dx_vec, du_vec;
+};
+
+// BF16 products grouped by ragged offsets (ragged.hip).  Strides in elements,
+// gs between groups.  Rows of the operands run along the group's tokens (a of
+// nt and nn, both operands of tn) or the group's own matrix (b of nt and nn).
+struct RaggedArgs {
+  const uint16_t *a, *b;
+  void* d;
+  const void* c;  // or NULL
+  const int32_t* offsets;
+  int64_t lda, ldb, b_gs, ldd, d_gs, ldc, c_gs;
+  int32_t G, M, N, K;  // nt, nn: d [M, N], contraction K; tn: M tokens, d [G, K, N]
+  int32_t c_f32, d_f32;
+  int32_t tiles_n, tiles_k;  // set by the launcher
+};
+
+enum RaggedLayout : int { RAGGED_NT = 0, RAGGED_NN = 1, RAGGED_TN = 2 };
+
 struct PackArgs {
   const float* x;
   int64_t sx_g, sx_r;
@@ -203,6 +275,15 @@ int64_t paged_attention_workspace(int64_t S, int64_t n, int64_t Hq, int64_t Hkv,
 // largest grid of the call's kernels
 int64_t paged_attention_grid(int64_t S, int64_t Hkv, int64_t row_tiles, int64_t D, int64_t cap);
 hipError_t launch_paged_attention(PagedAttnArgs p, hipStream_t stream);
+int64_t rms_norm_bwd_parts(int64_t rows, int64_t H);
+hipError_t launch_rms_norm(const RmsNormArgs& p, hipStream_t stream);
+hipError_t launch_rms_norm_bwd(const RmsNormBwdArgs& p, hipStream_t stream);
+int64_t swiglu_grid(int64_t rows, int64_t I);
+int64_t swiglu_bwd_grid(int64_t rows, int64_t I);
+hipError_t launch_swiglu(SwigluArgs p, hipStream_t stream);
+hipError_t launch_swiglu_bwd(const SwigluBwdArgs& p, hipStream_t stream);
+int64_t ragged_grid(int layout, int64_t G, int64_t M, int64_t N, int64_t K);
+hipError_t launch_ragged(RaggedArgs p, int layout, hipStream_t stream);
 hipError_t launch_per_block(const QuantArgs& p, hipStream_t stream);
 hipError_t launch_pack_ue8m0(const PackArgs& p, hipStream_t stream);
 

@@ -1,0 +1,255 @@
+// Root-mean-square norm with the residual's addition and FP8 output, and its
+// gradient, gfx950.
+//
+//   h   = x + residual, rounded to the residual's type (h = x without one)
+//   r   = 1 / sqrt(mean(h^2) + eps)
+//   y   = h r w                                     (FP32)
+//   out   y rounded to BF16 or F32, and / or q, sf: the 1x128 FP8 cast of the
+//         FP32 y (amax / 448 floored as the per-token cast does)
+//   gradient of the sum h, with g = w dy and xh = h r:
+//   dx  = dh + r (g - xh mean(g xh)),   dw = sum over rows of dy xh
+//
+// A row is held in registers by NT lanes, NI chunks of 8 elements each, chunk c
+// of the row in lane c % NT: 16 lanes hold one 128-element block of the cast,
+// whose maximum is reduced without shared memory.  Squares that leave FP32's
+// range (rows of values past 2^60) are taken again of h 2^-64.
+
+#include <type_traits>
+
+#include "launch.hpp"
+#include "rows.hpp"
+
+namespace dgmi {
+
+namespace {
+
+constexpr float TINY = 0x1p-64f;  // factor of rows whose squares overflow
+
+template <int NT>
+constexpr int rows_of() { return NT < 256 ? 256 / NT : 1; }  // rows a workgroup takes side by side
+
+template <int NT, int NI>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(const RmsNormArgs p) {
+  __shared__ float red[NT / 64 + 1];
+  const int lane = threadIdx.x % NT;
+  const int64_t row = (int64_t)blockIdx.x * rows_of<NT>() + threadIdx.x / NT;
+  if (row >= p.rows) return;  // (whole groups of NT lanes; NT > 64 has one row a workgroup)
+  const int64_t i0 = row / p.heads, i1 = row % p.heads;
+  float v[NI][8];
+  const int64_t ox = i0 * p.sx_0 + i1 * p.sx_1;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) load8(p.x, p.x_bf16, ox, (lane + i * NT) * 8, p.H, p.x_vec, v[i]);
+  if (p.res != nullptr) {
+    const int64_t orr = i0 * p.sr_0 + i1 * p.sr_1, oh = i0 * p.sh_0 + i1 * p.sh_1;
+    float t[NI][8];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) load8(p.res, p.r_bf16, orr, (lane + i * NT) * 8, p.H, p.r_vec, t[i]);
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[i][e] += t[i][e];
+      if (p.r_bf16) {  // the norm is of the sum as it is stored
+        const i32x4 w = round8(v[i]);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          v[i][2 * e] = __uint_as_float((uint32_t)w[e] << 16);
+          v[i][2 * e + 1] = __uint_as_float((uint32_t)w[e] & 0xffff0000u);
+        }
+      }
+      if (p.h != nullptr) store8(p.h, p.r_bf16, oh, (lane + i * NT) * 8, p.H, p.h_vec, v[i]);
+    }
+  }
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < NI; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) s = __builtin_fmaf(v[i][e], v[i][e], s);
+  s = row_sum<NT>(s, red);
+  float k = 1.0f;
+  if (!(s < INFINITY)) {  // (the whole row takes this turn)
+    k = TINY;
+    s = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s += (v[i][e] * TINY) * (v[i][e] * TINY);
+    s = row_sum<NT>(s, red);
+  }
+  const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(s, (float)p.H) + p.eps * k * k));
+  const int64_t oy = i0 * p.sy_0 + i1 * p.sy_1, oq = i0 * p.sq_0 + i1 * p.sq_1, os = i0 * p.ss_0 + i1 * p.ss_1;
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    const int at = (lane + i * NT) * 8;
+    float w[8];
+    load8(p.w, p.w_bf16, 0, at, p.H, p.w_vec, w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) w[e] *= (v[i][e] * k) * r;
+    if (p.y != nullptr) store8(p.y, p.y_bf16, oy, at, p.H, p.y_vec, w);
+    if (p.q == nullptr) continue;
+    uint32_t lo, hi;
+    const float sc = cast_block8(w, p.ue8m0, lo, hi);
+    if (at >= p.H) continue;
+    store_codes8(p.q + oq, at, p.H, p.q_vec, lo, hi);
+    if ((lane & 15) == 0) p.sf[os + (at >> 7) * p.ss_k] = sc;
+  }
+}
+
+// Rows blockIdx, + gridDim, ... of the gradient; the weight's sums stay in
+// registers and leave as one row of partial sums a workgroup.
+template <int NT, int NI>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_bwd_kernel(const RmsNormBwdArgs p) {
+  constexpr int RW = rows_of<NT>();
+  __shared__ float red[NT / 64 + 1];
+  __shared__ float part[RW > 1 ? RW * NT * NI * 8 : 1];
+  const int lane = threadIdx.x % NT, slot = threadIdx.x / NT;
+  float w[NI][8], dw[NI][8];
+#pragma unroll
+  for (int i = 0; i < NI; ++i) {
+    load8(p.w, p.w_bf16, 0, (lane + i * NT) * 8, p.H, p.w_vec, w[i]);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
+  }
+  for (int64_t row = (int64_t)blockIdx.x * RW + slot; row < p.rows; row += (int64_t)gridDim.x * RW) {
+    const int64_t i0 = row / p.heads, i1 = row % p.heads;
+    const int64_t oh = i0 * p.sh_0 + i1 * p.sh_1, og = i0 * p.sg_0 + i1 * p.sg_1;
+    float h[NI][8], g[NI][8];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      load8(p.h, p.h_bf16, oh, (lane + i * NT) * 8, p.H, p.h_vec, h[i]);
+      load8(p.dy, p.dy_bf16, og, (lane + i * NT) * 8, p.H, p.dy_vec, g[i]);
+    }
+    float s = 0.0f, m = 0.0f;
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        s = __builtin_fmaf(h[i][e], h[i][e], s);
+        m = __builtin_fmaf(g[i][e] * w[i][e], h[i][e], m);
+      }
+    s = row_sum<NT>(s, red);
+    m = row_sum<NT>(m, red);
+    float k = 1.0f;
+    if (!(s < INFINITY)) {
+      k = TINY;
+      s = m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          s += (h[i][e] * TINY) * (h[i][e] * TINY);
+          m += g[i][e] * w[i][e] * (h[i][e] * TINY);
+        }
+      s = row_sum<NT>(s, red);
+      m = row_sum<NT>(m, red);
+    }
+    const float rk = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(s, (float)p.H) + p.eps * k * k));
+    const float r = rk * k;                        // h r = (h k) rk
+    const float mean = __fdiv_rn(m * rk, (float)p.H);  // of g xh
+    const int64_t od = i0 * p.sd_0 + i1 * p.sd_1, ox = i0 * p.sx_0 + i1 * p.sx_1;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int at = (lane + i * NT) * 8;
+      float dx[8];
+      load8(p.dh != nullptr ? p.dh : p.h, p.dh_bf16, od, at, p.dh != nullptr ? p.H : 0, p.dh_vec, dx);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float xh = (h[i][e] * k) * rk;
+        dw[i][e] = __builtin_fmaf(g[i][e], xh, dw[i][e]);
+        dx[e] = __builtin_fmaf(r, __builtin_fmaf(-xh, mean, g[i][e] * w[i][e]), dx[e]);
+      }
+      store8(p.dx, p.dx_bf16, ox, at, p.H, p.dx_vec, dx);
+    }
+  }
+  if (p.part == nullptr) return;
+  float* to = p.part + (int64_t)blockIdx.x * p.H;
+  if constexpr (RW > 1) {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) part[slot * NT * NI * 8 + (lane + i * NT) * 8 + e] = dw[i][e];
+    __syncthreads();
+    for (int c = threadIdx.x; c < p.H; c += 256) {
+      float t = 0.0f;
+      for (int o = 0; o < RW; ++o) t += part[o * NT * NI * 8 + c];
+      to[c] = t;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NI; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if ((lane + i * NT) * 8 + e < p.H) to[(lane + i * NT) * 8 + e] = dw[i][e];
+  }
+}
+
+// The weight's gradient from the partial rows, in their order: 32 columns a
+// workgroup, 32 runs of partial rows side by side.
+__global__ __launch_bounds__(1024) void rms_norm_bwd_weight_kernel(const float* part, int parts, int H, void* dw,
+                                                                   int bf16) {
+  __shared__ float sums[32][33];
+  const int c = blockIdx.x * 32 + (threadIdx.x & 31), run = threadIdx.x >> 5;
+  const int per = (parts + 31) / 32;
+  float s = 0.0f;
+  if (c < H) {
+    const int end = min(parts, (run + 1) * per);
+    for (int i = run * per; i < end; ++i) s += part[(int64_t)i * H + c];
+  }
+  sums[run][threadIdx.x & 31] = s;
+  __syncthreads();
+  if (run == 0 && c < H) {
+    s = 0.0f;
+    for (int i = 0; i < 32; ++i) s += sums[i][threadIdx.x];
+    if (bf16) static_cast<uint16_t*>(dw)[c] = f32_to_bf16_rne(s);
+    else static_cast<float*>(dw)[c] = s;
+  }
+}
+
+// Lanes and chunks that hold a row of H: NT * NI * 8 >= H.
+template <class F>
+hipError_t with_row_shape(int64_t H, F f) {
+#define DGMI_ROW(NT_, NI_) \
+  if (H <= (int64_t)NT_ * NI_ * 8) return f(std::integral_constant<int, NT_>{}, std::integral_constant<int, NI_>{})
+  DGMI_ROW(16, 1);
+  DGMI_ROW(32, 1);
+  DGMI_ROW(64, 1);
+  DGMI_ROW(64, 2);
+  DGMI_ROW(256, 1);
+  DGMI_ROW(512, 1);
+  DGMI_ROW(512, 2);
+  DGMI_ROW(1024, 2);
+#undef DGMI_ROW
+  return hipErrorInvalidValue;
+}
+
+}  // namespace
+
+// Partial rows of the weight's gradient: workgroups of the gradient kernel.
+int64_t rms_norm_bwd_parts(int64_t rows, int64_t H) {
+  const int64_t per = H <= 128 ? 16 : H <= 256 ? 8 : H <= 1024 ? 4 : 1;  // rows a workgroup takes side by side
+  const int64_t groups = (rows + per - 1) / per;
+  return groups < 512 ? groups : 512;
+}
+
+hipError_t launch_rms_norm(const RmsNormArgs& p, hipStream_t stream) {
+  return with_row_shape(p.H, [&](auto nt, auto ni) {
+    constexpr int NT = decltype(nt)::value, NI = decltype(ni)::value;
+    const int64_t blocks = (p.rows + rows_of<NT>() - 1) / rows_of<NT>();
+    rms_norm_kernel<NT, NI><<<dim3((unsigned)blocks), dim3(NT < 256 ? 256 : NT), 0, stream>>>(p);
+    return hipGetLastError();
+  });
+}
+
+hipError_t launch_rms_norm_bwd(const RmsNormBwdArgs& p, hipStream_t stream) {
+  const int64_t parts = rms_norm_bwd_parts(p.rows, p.H);
+  const hipError_t e = parts == 0 ? hipSuccess : with_row_shape(p.H, [&](auto nt, auto ni) {
+    constexpr int NT = decltype(nt)::value, NI = decltype(ni)::value;
+    rms_norm_bwd_kernel<NT, NI><<<dim3((unsigned)parts), dim3(NT < 256 ? 256 : NT), 0, stream>>>(p);
+    return hipGetLastError();
+  });
+  if (e != hipSuccess || p.dw == nullptr) return e;
+  rms_norm_bwd_weight_kernel<<<dim3((unsigned)((p.H + 31) / 32)), dim3(1024), 0, stream>>>(p.part, (int)parts, p.H,
+                                                                                          p.dw, p.dw_bf16);
+  return hipGetLastError();
+}
+
+}  // namespace dgmi

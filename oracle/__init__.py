@@ -22,6 +22,8 @@ Modules
   router   -- expert routing (scores, groups, top-k, weights) and its gradient.
   attention -- the paged FP8 key/value cache: append with the position
              rotation, attention over it.
+  layer    -- the norm with the residual's addition, the gated activation,
+             their gradients, and the products of ragged groups.
 
 Sources (the pages this follows):
   * "DeepInside DeepGEMM: Unpacking DeepSeek's Unified Tensor Core Library
