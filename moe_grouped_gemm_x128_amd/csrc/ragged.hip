@@ -31,12 +31,14 @@ constexpr int SLICE = 64;  // contraction elements of a stage
 constexpr int XCDS = 8;
 
 typedef __attribute__((address_space(3))) void lds_t;
-typedef __bf16 bf16x4v __attribute__((ext_vector_type(4)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 
-// K-major stage: 16-byte chunk c of tile row r lies at slot c ^ h(r); the 16 rows
-// of a fragment read at one chunk then hit distinct banks.
-__device__ __host__ constexpr int row_swz(int r) { return ((r ^ (r >> 3)) & 1) | (r & 6); }
+// K-major stage: 16-byte chunk c of tile row r lies at slot c ^ h(r), h linear over
+// GF(2) in the bits of r: the 16 rows of a fragment, consecutive or in PERM's order
+// (bits 0, 1, 4 and 5), read at one chunk hit distinct banks.
+__device__ __host__ constexpr int row_swz(int r) {
+  return ((r ^ (r >> 3) ^ (r >> 5)) & 1) | (r & 2) | ((((r >> 2) ^ (r >> 4)) & 1) << 2);
+}
 // MN-major stage: chunk c of contraction row k lies at slot c ^ hk(k): the four
 // rows of each of two lane groups that read together hit distinct banks.
 __device__ __host__ constexpr int col_swz(int k) { return 2 * ((k & 3) | ((((k >> 3) ^ (k >> 4)) & 1) << 2)); }
@@ -47,6 +49,12 @@ struct Shape {
   static constexpr int NW = WM * WN, NT = NW * 64;
   static constexpr int TM = BM / WM, TN = BN / WN, FM = TM / 16, FN = TN / 16;
 };
+
+// s_waitcnt operand: all LDS traffic done, and all but the last n loads.
+constexpr int vmcnt_lgkm0(int n) { return (n & 15) | ((n >> 4) << 14) | (7 << 4); }
+
+__device__ __forceinline__ bf16x8 lo_bf16(const i32x8& v) { return __builtin_bit_cast(bf16x8, i32x4{v[0], v[1], v[2], v[3]}); }
+__device__ __forceinline__ bf16x8 hi_bf16(const i32x8& v) { return __builtin_bit_cast(bf16x8, i32x4{v[4], v[5], v[6], v[7]}); }
 
 // First row and end of group g, inside [0, M].
 __device__ __forceinline__ void group_rows(const int32_t* offsets, int g, int M, int& first, int& end) {
@@ -157,63 +165,119 @@ __global__ __launch_bounds__(T::NT) void ragged_kernel(const RaggedArgs p) {
   }
   const int KB = (len + SLICE - 1) / SLICE;
 
-  // loads of slice kb into a stage, 1024 bytes a wave and instruction.  K-major: 8 tile rows of 128 bytes;
-  // the resource ends after the last row that exists, and what lies past it reads as zero.
-  auto load_rows = [&](uint8_t* stage, const uint16_t* base, int64_t ld, int rows, int kb, auto tile_rows) {
-    constexpr int R = decltype(tile_rows)::value;
-    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)base, (short)0, (int)(min(max(rows, 0), R) * ld * 2), 0x00020000);
-#pragma unroll
-    for (int j = 0; j < R / (8 * T::NW); ++j) {
-      const int r = (j * T::NW + wave) * 8 + (lane >> 3);
-      const uint32_t off = (uint32_t)(r * ld * 2) + (uint32_t)(((lane & 7) ^ row_swz(r)) << 4);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_t*)(stage + (j * T::NW + wave) * 1024), 16, off,
-                                               kb * SLICE * 2, 0, 0);
-    }
+  // One load of a slice into a stage, 1024 bytes a wave.  K-major: load j fills 8 tile rows of 128 bytes; its
+  // resource ends after the last row that exists, what lies past it reads as zero.  A slice past the last one has an
+  // empty resource: zeros, no memory access.
+  constexpr int A_LD = A_STAGE / (1024 * T::NW), B_LD = B_STAGE / (1024 * T::NW);  // loads of a slice, per wave
+  const int lrow = lane >> 3;
+  const uint32_t vchunk = (uint32_t)((lane & 7) ^ lrow);  // (row_swz of 8 j + lrow is row_swz(8 j) ^ lrow)
+  auto rows_vrow = [&](int64_t ld) { return (uint32_t)((wave * 8 + lrow) * ld * 2); };
+  auto rows_size = [&](int64_t ld, int rows, int j) {
+    return __builtin_amdgcn_readfirstlane((int)(max(0, min(rows - j * T::NW * 8, T::NW * 8)) * ld * 2));
   };
-  // MN-major: SLICE contraction rows of W columns; rows past `len` read as zero (the resource is the slice's own and
-  // ends with the 16-byte chunk of the last column of the last row), columns past the operand's feed outputs that
-  // are never stored.
-  auto load_cols = [&](uint8_t* stage, const uint16_t* base, int64_t ld, int cols, int kb, auto width) {
+  auto load_rows_one = [&](uint8_t* stage, const uint16_t* base, int64_t ld, uint32_t vrow, int size, int kb, int j) {
+    const uint32_t hu = (uint32_t)row_swz((j * T::NW + wave) * 8);
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)(base + (int64_t)j * T::NW * 8 * ld), (short)0, kb < KB ? size : 0, 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_t*)(stage + (j * T::NW + wave) * 1024), 16,
+                                             vrow + ((vchunk ^ hu) << 4), kb * SLICE * 2, 0, 0);
+  };
+  // MN-major: load j fills PER contraction rows of W columns.  Rows past `len` read as zero (the resource starts at
+  // the slice and ends with the 16-byte chunk of the last column of the last row), columns past the operand's feed
+  // outputs that are never stored.
+  struct Cols {
+    const uint8_t* at;  // the next slice to load
+    int64_t left;       // bytes from there to the operand's end
+    int64_t step;
+  };
+  auto cols_of = [&](const uint16_t* base, int64_t ld, int cols) {
+    return Cols{reinterpret_cast<const uint8_t*>(base), len > 0 ? ((len - 1) * ld + (cols + 7) / 8 * 8) * 2 : 0, SLICE * ld * 2};
+  };
+  auto load_cols_one = [&](uint8_t* stage, const Cols& c, const uint32_t* voff, int j) {
+    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
+        (void*)c.at, (short)0, (int)min(max(c.left, (int64_t)0), (int64_t)0x7fffffff), 0x00020000);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_t*)(stage + (j * T::NW + wave) * 1024), 16, voff[j], 0, 0, 0);
+  };
+  auto cols_voff = [&](int64_t ld, int j, auto width) {
     constexpr int W = decltype(width)::value, SLOTS = W / 8, PER = 64 / SLOTS;
-    const int left = len - kb * SLICE;
-    const int64_t bytes = left > 0 && cols > 0 ? ((int64_t)(left - 1) * ld + (cols + 7) / 8 * 8) * 2 : 0;
-    const __amdgpu_buffer_rsrc_t rsrc = __builtin_amdgcn_make_buffer_rsrc(
-        (void*)(base + (int64_t)kb * SLICE * ld), (short)0, (int)min(bytes, (int64_t)0x7fffffff), 0x00020000);
+    const int k = (j * T::NW + wave) * PER + lane / SLOTS;
+    return (uint32_t)(k * ld * 2) + (uint32_t)(((lane % SLOTS) ^ col_swz(k)) << 4);
+  };
+  int a_size[A_LD], b_size[B_LD];
+  uint32_t a_voff[A_LD], b_voff[B_LD];
+  Cols a_cols = {}, b_cols = {};
 #pragma unroll
-    for (int j = 0; j < SLICE / (PER * T::NW); ++j) {
-      const int k = (j * T::NW + wave) * PER + lane / SLOTS;
-      const uint32_t off = (uint32_t)(k * ld * 2) + (uint32_t)(((lane % SLOTS) ^ col_swz(k)) << 4);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rsrc, (lds_t*)(stage + (j * T::NW + wave) * 1024), 16, off, 0, 0, 0);
+  for (int j = 0; j < A_LD; ++j) {
+    if constexpr (A_MN) a_voff[j] = cols_voff(p.lda, j, std::integral_constant<int, T::BM>{});
+    else a_size[j] = rows_size(p.lda, m_end - m0, j);
+  }
+#pragma unroll
+  for (int j = 0; j < B_LD; ++j) {
+    if constexpr (B_MN) b_voff[j] = cols_voff(p.ldb, j, std::integral_constant<int, T::BN>{});
+    else b_size[j] = rows_size(p.ldb, n_end - n0, j);
+  }
+  if constexpr (A_MN) a_cols = cols_of(A, p.lda, m_end - m0);
+  if constexpr (B_MN) b_cols = cols_of(B, p.ldb, n_end - n0);
+  const uint32_t a_vrow = rows_vrow(p.lda), b_vrow = rows_vrow(p.ldb);
+  auto load_a_one = [&](uint8_t* stage, int kb, int j) {
+    if constexpr (A_MN) {
+      load_cols_one(stage, a_cols, a_voff, j);
+      if (j + 1 == A_LD) a_cols.at += a_cols.step, a_cols.left -= a_cols.step;
+    } else {
+      load_rows_one(stage, A, p.lda, a_vrow, a_size[j], kb, j);
     }
   };
-  auto load = [&](uint8_t* sa, uint8_t* sb, int kb) {
-    if constexpr (A_MN) load_cols(sa, A, p.lda, m_end - m0, kb, std::integral_constant<int, T::BM>{});
-    else load_rows(sa, A, p.lda, m_end - m0, kb, std::integral_constant<int, T::BM>{});
-    if constexpr (B_MN) load_cols(sb, B, p.ldb, n_end - n0, kb, std::integral_constant<int, T::BN>{});
-    else load_rows(sb, B, p.ldb, n_end - n0, kb, std::integral_constant<int, T::BN>{});
+  auto load_b_one = [&](uint8_t* stage, int kb, int j) {
+    if constexpr (B_MN) {
+      load_cols_one(stage, b_cols, b_voff, j);
+      if (j + 1 == B_LD) b_cols.at += b_cols.step, b_cols.left -= b_cols.step;
+    } else {
+      load_rows_one(stage, B, p.ldb, b_vrow, b_size[j], kb, j);
+    }
+  };
+  auto load_a = [&](uint8_t* stage, int kb) {
+#pragma unroll
+    for (int j = 0; j < A_LD; ++j) load_a_one(stage, kb, j);
+  };
+  auto load_b = [&](uint8_t* stage, int kb) {
+#pragma unroll
+    for (int j = 0; j < B_LD; ++j) load_b_one(stage, kb, j);
   };
 
-  // fragments: 16 tile rows (columns) at r0, contraction 32 half + 8 (lane / 16) .. +7 in lane (row lane % 16)
+  // Fragments of a slice: 16 tile rows (columns) from r0, contraction 32 half + 8 (lane / 16) .. +7 in lane (row
+  // lane % 16), half 0 in the first four registers.  With PERM the rows of B's fragment f are permuted so that a lane
+  // ends up with 16 consecutive columns of the output.
   const int fr = lane & 15, q = lane >> 4;
-  auto frag_rows = [&](const uint8_t* stage, int r0, int half) {
-    const int r = r0 + fr;
-    return *reinterpret_cast<const bf16x8*>(stage + r * 128 + (((half * 4 + q) ^ row_swz(r)) << 4));
+  auto frag_rows = [&](const uint8_t* stage, int r) {
+    const int off = r * 128 + ((q ^ row_swz(r)) << 4);
+    const i32x4 l = *reinterpret_cast<const i32x4*>(stage + off), h = *reinterpret_cast<const i32x4*>(stage + (off ^ 64));
+    return i32x8{l[0], l[1], l[2], l[3], h[0], h[1], h[2], h[3]};
   };
   // lane s of a group of 16 reads 4 columns of contraction row 8 q + 4 t + s / 4; transposed, the group hands lane
   // s the four rows of column s
-  auto frag_cols = [&](const uint8_t* stage, int r0, int half, auto width) {
+  auto frag_cols = [&](const uint8_t* stage, int r0, auto width) {
     constexpr int W = decltype(width)::value;
     typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-    union { bf16x8 v; s16x4 h[2]; } u;
+    i32x8 v;
 #pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int k = half * 32 + 8 * q + 4 * t + (fr >> 2);
+    for (int t = 0; t < 4; ++t) {
+      const int k = (t >> 1) * 32 + 8 * q + 4 * (t & 1) + (fr >> 2);
       const int chunk = r0 / 8 + ((fr >> 1) & 1);
-      u.h[t] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (lds_s16x4*)(stage + k * W * 2 + ((chunk ^ col_swz(k)) << 4) + 8 * (fr & 1)));
+      const i32x2 x = __builtin_bit_cast(i32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (lds_s16x4*)(stage + k * W * 2 + ((chunk ^ col_swz(k)) << 4) + 8 * (fr & 1))));
+      v[2 * t] = x[0];
+      v[2 * t + 1] = x[1];
     }
-    return u.v;
+    return v;
+  };
+  constexpr bool PERM = !B_MN && T::TN == 64;
+  auto a_frag = [&](const uint8_t* stage, int i) {
+    if constexpr (A_MN) return frag_cols(stage, wm * T::TM + 16 * i, std::integral_constant<int, T::BM>{});
+    else return frag_rows(stage, wm * T::TM + 16 * i + fr);
+  };
+  auto b_frag = [&](const uint8_t* stage, int f) {
+    if constexpr (B_MN) return frag_cols(stage, wn * T::TN + 16 * f, std::integral_constant<int, T::BN>{});
+    else return frag_rows(stage, wn * T::TN + (PERM ? (fr >> 2) * 16 + f * 4 + (fr & 3) : 16 * f + fr));
   };
   f32x4 acc[T::FM][T::FN];
 #pragma unroll
@@ -221,81 +285,126 @@ __global__ __launch_bounds__(T::NT) void ragged_kernel(const RaggedArgs p) {
 #pragma unroll
     for (int f = 0; f < T::FN; ++f) acc[i][f] = f32x4{0.f, 0.f, 0.f, 0.f};
   const bool live = m0 + wm * T::TM < m_end && n0 + wn * T::TN < n_end;  // else nothing of the wave is stored
-  auto compute = [&](const uint8_t* sa, const uint8_t* sb) {
-    if (!live) return;
+
+  // One software pipeline over the fragment rows of all slices, two barriers a slice.  Early, before the second
+  // fragment row: every wave has the slice's B fragments in registers, so the B part of its stage takes slice kb + 2.
+  // Late, before the last one: the next slice has landed and every wave is done with this one's A part, which takes
+  // slice kb + 2; the next slice's first fragments are read while the last MFMAs run.  The loads of a point go out one
+  // after each MFMA that follows it.  Waiting loads in issue order: B of kb + 2 may stay in flight at the late point.
+  auto meet = [&](auto loads) {  // all but the wave's last `loads` loads have landed, in every wave
+    __builtin_amdgcn_s_waitcnt(vmcnt_lgkm0(decltype(loads)::value));
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");  // (no access moves past it)
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto early = [&]() { meet(std::integral_constant<int, 63>{}); };
+  auto late = [&]() { meet(std::integral_constant<int, B_LD>{}); };
+  if (KB > 0) {
+    load_a(lds_a0, 0);
+    load_b(lds_b0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+    load_b(lds_b1, 1);
+    load_a(lds_a1, 1);
+    __builtin_amdgcn_sched_barrier(0);
+    meet(std::integral_constant<int, A_LD + B_LD>{});
+    if (live) {
+      i32x8 bf[T::FN], af;
 #pragma unroll
-    for (int half = 0; half < 2; ++half) {
-      bf16x8 bf[T::FN];
+      for (int f = 0; f < T::FN; ++f) bf[f] = b_frag(lds_b0, f);
+      af = a_frag(lds_a0, 0);
+      auto slice = [&](uint8_t* cur_a, uint8_t* cur_b, const uint8_t* nxt_a, const uint8_t* nxt_b, int kb) {
 #pragma unroll
-      for (int f = 0; f < T::FN; ++f) {
-        if constexpr (B_MN) bf[f] = frag_cols(sb, wn * T::TN + 16 * f, half, std::integral_constant<int, T::BN>{});
-        else bf[f] = frag_rows(sb, wn * T::TN + 16 * f, half);
+        for (int i = 0; i < T::FM; ++i) {
+          __builtin_amdgcn_sched_barrier(0);
+          if (i == 1) early();
+          if (i + 1 == T::FM) late();
+          const i32x8 next = i + 1 < T::FM ? a_frag(cur_a, i + 1) : a_frag(nxt_a, 0);
+#pragma unroll
+          for (int f = 0; f < T::FN; ++f) {
+            __builtin_amdgcn_sched_barrier(0);
+            acc[i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(lo_bf16(bf[f]), lo_bf16(af), acc[i][f], 0, 0, 0);
+#pragma unroll
+            for (int j = f; j < (i == 1 ? B_LD : i + 1 == T::FM ? A_LD : 0); j += T::FN) {
+              if (i == 1) load_b_one(cur_b, kb + 2, j);
+              else load_a_one(cur_a, kb + 2, j);
+            }
+          }
+#pragma unroll
+          for (int f = 0; f < T::FN; ++f) {
+            __builtin_amdgcn_sched_barrier(0);
+            acc[i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(hi_bf16(bf[f]), hi_bf16(af), acc[i][f], 0, 0, 0);
+          }
+          if (i + 1 == T::FM) {
+#pragma unroll
+            for (int f = 0; f < T::FN; ++f) bf[f] = b_frag(nxt_b, f);
+          }
+          af = next;
+        }
+      };
+      int kb = 0;
+      for (; kb + 2 <= KB; kb += 2) {
+        slice(lds_a0, lds_b0, lds_a1, lds_b1, kb);
+        slice(lds_a1, lds_b1, lds_a0, lds_b0, kb + 1);
       }
-#pragma unroll
-      for (int i = 0; i < T::FM; ++i) {
-        bf16x8 af;
-        if constexpr (A_MN) af = frag_cols(sa, wm * T::TM + 16 * i, half, std::integral_constant<int, T::BM>{});
-        else af = frag_rows(sa, wm * T::TM + 16 * i, half);
-#pragma unroll
-        for (int f = 0; f < T::FN; ++f) acc[i][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(bf[f], af, acc[i][f], 0, 0, 0);
+      if (kb < KB) slice(lds_a0, lds_b0, lds_a1, lds_b1, kb);
+    } else {
+      for (int kb = 0; kb < KB; ++kb) {  // (loads and barriers only)
+        early();
+        load_b(kb & 1 ? lds_b1 : lds_b0, kb + 2);
+        late();
+        load_a(kb & 1 ? lds_a1 : lds_a0, kb + 2);
       }
     }
-  };
-  // every wave's loads have landed and its reads of the other stage are done
-  auto ready = [&]() {
-    __builtin_amdgcn_s_waitcnt(0);
-    __syncthreads();
-  };
-  if (KB > 0) load(lds_a0, lds_b0, 0);
-  for (int kb = 0; kb < KB; kb += 2) {
-    ready();
-    if (kb + 1 < KB) load(lds_a1, lds_b1, kb + 1);
-    compute(lds_a0, lds_b0);
-    if (kb + 1 < KB) {
-      ready();
-      if (kb + 2 < KB) load(lds_a0, lds_b0, kb + 2);
-      compute(lds_a1, lds_b1);
-    }
+    __builtin_amdgcn_s_waitcnt(0);  // (no load may write LDS after the workgroup's end)
   }
   if (!live) return;
 
-  // lane: output row lane % 16 and columns 4 (lane / 16) .. +3 of each fragment
+  // lane: output row lane % 16 of each fragment row and, PERM, 16 consecutive columns, else 4 of each fragment
   const int64_t d_at = LAY == RAGGED_TN ? (int64_t)g * p.d_gs : 0, c_at = LAY == RAGGED_TN ? (int64_t)g * p.c_gs : 0;
+  constexpr int RUN = PERM ? 16 : 4;  // consecutive columns of a lane
 #pragma unroll
   for (int i = 0; i < T::FM; ++i) {
     const int row = m0 + wm * T::TM + 16 * i + fr;
     if (row >= m_end) continue;
 #pragma unroll
-    for (int f = 0; f < T::FN; ++f) {
-      const int col = n0 + wn * T::TN + 16 * f + 4 * q;
-      f32x4 v = acc[i][f];
-      const int n = min(4, n_end - col);
+    for (int f0 = 0; f0 < T::FN; f0 += RUN / 4) {
+      const int col = n0 + wn * T::TN + (PERM ? 16 * q : 16 * f0 + 4 * q);
+      const int n = min(RUN, n_end - col);
       if (p.c != nullptr) {
         const int64_t at = c_at + (int64_t)row * p.ldc + col;
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (e < n) v[e] += p.c_f32 ? static_cast<const float*>(p.c)[at + e]
-                                     : bf16_to_f32(static_cast<const uint16_t*>(p.c)[at + e]);
+        for (int e = 0; e < RUN; ++e)
+          if (e < n) acc[i][f0 + e / 4][e & 3] += p.c_f32 ? static_cast<const float*>(p.c)[at + e]
+                                                          : bf16_to_f32(static_cast<const uint16_t*>(p.c)[at + e]);
       }
       const int64_t at = d_at + (int64_t)row * p.ldd + col;
       if constexpr (F32) {
         float* to = static_cast<float*>(p.d) + at;
-        if (n == 4 && (reinterpret_cast<uintptr_t>(to) & 15) == 0) {
-          *reinterpret_cast<f32x4*>(to) = v;
+        if (n == RUN && (reinterpret_cast<uintptr_t>(to) & 15) == 0) {
+#pragma unroll
+          for (int e = 0; e < RUN; e += 4) *reinterpret_cast<f32x4*>(to + e) = acc[i][f0 + e / 4];
         } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (e < n) to[e] = v[e];
+          for (int e = 0; e < RUN; ++e)
+            if (e < n) to[e] = acc[i][f0 + e / 4][e & 3];
         }
       } else {
         uint16_t* to = static_cast<uint16_t*>(p.d) + at;
-        const i32x2 w = to_bf16x4_bits(v);
-        if (n == 4 && (reinterpret_cast<uintptr_t>(to) & 7) == 0) {
-          *reinterpret_cast<i32x2*>(to) = w;
+        i32x2 w[RUN / 4];
+#pragma unroll
+        for (int e = 0; e < RUN / 4; ++e) w[e] = to_bf16x4_bits(acc[i][f0 + e]);
+        if (n == RUN && (reinterpret_cast<uintptr_t>(to) & (PERM ? 15 : 7)) == 0) {
+          if constexpr (PERM) {
+#pragma unroll
+            for (int e = 0; e < RUN / 4; e += 2)
+              *reinterpret_cast<i32x4*>(to + 4 * e) = i32x4{w[e][0], w[e][1], w[e + 1][0], w[e + 1][1]};
+          } else {
+            *reinterpret_cast<i32x2*>(to) = w[0];
+          }
         } else {
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (e < n) to[e] = (uint16_t)((uint32_t)w[e / 2] >> (16 * (e & 1)));
+          for (int e = 0; e < RUN; ++e)
+            if (e < n) to[e] = (uint16_t)((uint32_t)w[e / 4][(e & 3) / 2] >> (16 * (e & 1)));
         }
       }
     }
