@@ -282,7 +282,8 @@ int64_t swiglu_grid(int64_t rows, int64_t I);
 int64_t swiglu_bwd_grid(int64_t rows, int64_t I);
 hipError_t launch_swiglu(SwigluArgs p, hipStream_t stream);
 hipError_t launch_swiglu_bwd(const SwigluBwdArgs& p, hipStream_t stream);
-int64_t ragged_grid(int layout, int64_t G, int64_t M, int64_t N, int64_t K);
+// tiles of a call at most (a kernel counts them in 31 bits)
+int64_t ragged_tiles(int layout, int64_t G, int64_t M, int64_t N, int64_t K);
 hipError_t launch_ragged(RaggedArgs p, int layout, hipStream_t stream);
 hipError_t launch_per_block(const QuantArgs& p, hipStream_t stream);
 hipError_t launch_pack_ue8m0(const PackArgs& p, hipStream_t stream);

@@ -101,6 +101,7 @@ def test_accumulate(form, dt, ct):
     ([1] + [0] * 300 + [2], 16, 64),
     ([512, 1, 1023, 256], 300, 704),             # several tiles a group, odd slices
     ([2047], 264, 1024),
+    ([64, 65, 128], 256, 4096),                  # rows a multiple of 4 KB apart: slices taken in turns
     ([90, 10, 300], 1, 64),                      # one column
     ([100, 29], 64, 2048),
 ])
@@ -120,6 +121,30 @@ def test_few_slices(K):
     """Every phase of the pipeline over the contraction, no slice among them."""
     for form in ("nt", "nn"):
         _case(form, [5, 260], 264, K, F32, F32 if K == 0 else None)
+
+
+@pytest.mark.parametrize("form", ["nt", "nn"])
+@pytest.mark.parametrize("sizes,N,K", [
+    ([1500, 3, 0, 1200, 129, 257, 2000], 4104, 128),   # more tiles than compute units: several a workgroup
+    ([4096], 4096, 64),                                # one slice, whole tiles
+    ([70] * 50 + [700], 3008, 192),                    # an odd number of slices, last tiles of every fill
+])
+def test_large_tiles(form, sizes, N, K):
+    _case(form, sizes, N, K, BF, None, first=2, behind=3)
+    _case(form, sizes, N, K, F32, BF)
+
+
+@pytest.mark.parametrize("sizes,N,K", [([40, 0, 200, 1, 64, 129], 2048, 2040), ([300, 65, 3, 10], 2056, 2048)])
+def test_large_tiles_of_weight_gradients(sizes, N, K):
+    _case("tn", sizes, N, K, F32, None, first=1)
+    _case("tn", sizes, N, K, BF, F32, behind=2)
+
+
+@pytest.mark.parametrize("form", ["nt", "nn", "tn"])
+@pytest.mark.parametrize("sizes", [[900, 500, 0, 1100], [130] * 30])
+def test_medium_tiles(form, sizes):
+    _case(form, sizes, 1032, 576, BF, None, first=1, behind=1)
+    _case(form, sizes, 1032, 512, F32, "in place")
 
 
 def test_offsets_out_of_range():
