@@ -216,7 +216,6 @@ struct SwigluArgs {
   int64_t sx_g, sx_r, sy_g, sy_r, sq_g, sq_r, ss_g, ss_r, ss_k, sw;
   int32_t G, R, I;
   int32_t x_bf16, y_bf16, x_vec, u_vec, y_vec, q_vec, ue8m0;
-  int32_t blocks;  // set by the launcher: 128-element blocks of a row
 };
 
 struct SwigluBwdArgs {
@@ -280,7 +279,7 @@ hipError_t launch_rms_norm(const RmsNormArgs& p, hipStream_t stream);
 hipError_t launch_rms_norm_bwd(const RmsNormBwdArgs& p, hipStream_t stream);
 int64_t swiglu_grid(int64_t rows, int64_t I);
 int64_t swiglu_bwd_grid(int64_t rows, int64_t I);
-hipError_t launch_swiglu(SwigluArgs p, hipStream_t stream);
+hipError_t launch_swiglu(const SwigluArgs& p, hipStream_t stream);
 hipError_t launch_swiglu_bwd(const SwigluBwdArgs& p, hipStream_t stream);
 // tiles of a call at most (a kernel counts them in 31 bits)
 int64_t ragged_tiles(int layout, int64_t G, int64_t M, int64_t N, int64_t K);

@@ -100,6 +100,7 @@ template <int NT, int NI>
 __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_bwd_kernel(const RmsNormBwdArgs p) {
   constexpr int RW = rows_of<NT>();
   __shared__ float red[NT / 64 + 1];
+  __shared__ float sums[2][2][NT / 64 + 1];
   __shared__ float part[RW > 1 ? RW * NT * NI * 8 : 1];
   const int lane = threadIdx.x % NT, slot = threadIdx.x / NT;
   float w[NI][8], dw[NI][8];
@@ -109,41 +110,57 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_bwd_kernel(const
 #pragma unroll
     for (int e = 0; e < 8; ++e) dw[i][e] = 0.0f;
   }
-  for (int64_t row = (int64_t)blockIdx.x * RW + slot; row < p.rows; row += (int64_t)gridDim.x * RW) {
-    const int64_t i0 = row / p.heads, i1 = row % p.heads;
+  const int64_t step = (int64_t)gridDim.x * RW;
+  int turn = 0;
+  for (int64_t row = (int64_t)blockIdx.x * RW + slot; row < p.rows; row += step, turn ^= 1) {
+    const int64_t i0 = row / p.heads, i1 = row - i0 * p.heads;
     const int64_t oh = i0 * p.sh_0 + i1 * p.sh_1, og = i0 * p.sg_0 + i1 * p.sg_1;
-    float h[NI][8], g[NI][8];
+    float x[NI][8], dy[NI][8];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      load8(p.h, p.h_bf16, oh, (lane + i * NT) * 8, p.H, p.h_vec, h[i]);
-      load8(p.dy, p.dy_bf16, og, (lane + i * NT) * 8, p.H, p.dy_vec, g[i]);
+      load8(p.h, p.h_bf16, oh, (lane + i * NT) * 8, p.H, p.h_vec, x[i]);
+      load8(p.dy, p.dy_bf16, og, (lane + i * NT) * 8, p.H, p.dy_vec, dy[i]);
     }
     float s = 0.0f, m = 0.0f;
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        s = __builtin_fmaf(h[i][e], h[i][e], s);
-        m = __builtin_fmaf(g[i][e] * w[i][e], h[i][e], m);
+        s = __builtin_fmaf(x[i][e], x[i][e], s);
+        m = __builtin_fmaf(dy[i][e] * w[i][e], x[i][e], m);
       }
-    s = row_sum<NT>(s, red);
-    m = row_sum<NT>(m, red);
+    s = lanes_sum<NT < 64 ? NT : 64>(s);
+    m = lanes_sum<NT < 64 ? NT : 64>(m);
+    if constexpr (NT > 64) {
+      // both sums in one exchange (a slot is written again two rows on, past a barrier that follows its reads)
+      if ((threadIdx.x & 63) == 0) {
+        sums[turn][0][threadIdx.x >> 6] = s;
+        sums[turn][1][threadIdx.x >> 6] = m;
+      }
+      __syncthreads();
+      s = m = 0.0f;
+#pragma unroll
+      for (int v = 0; v < NT / 64; ++v) {
+        s += sums[turn][0][v];
+        m += sums[turn][1][v];
+      }
+    }
     float k = 1.0f;
-    if (!(s < INFINITY)) {
+    if (!(s < INFINITY)) {  // (the whole row takes this turn)
       k = TINY;
       s = m = 0.0f;
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          s += (h[i][e] * TINY) * (h[i][e] * TINY);
-          m += g[i][e] * w[i][e] * (h[i][e] * TINY);
+          s += (x[i][e] * TINY) * (x[i][e] * TINY);
+          m += dy[i][e] * w[i][e] * (x[i][e] * TINY);
         }
       s = row_sum<NT>(s, red);
       m = row_sum<NT>(m, red);
     }
     const float rk = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(s, (float)p.H) + p.eps * k * k));
-    const float r = rk * k;                        // h r = (h k) rk
+    const float r = rk * k;                            // h r = (h k) rk
     const float mean = __fdiv_rn(m * rk, (float)p.H);  // of g xh
     const int64_t od = i0 * p.sd_0 + i1 * p.sd_1, ox = i0 * p.sx_0 + i1 * p.sx_1;
 #pragma unroll
@@ -153,9 +170,9 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_bwd_kernel(const
       load8(p.dh != nullptr ? p.dh : p.h, p.dh_bf16, od, at, p.dh != nullptr ? p.H : 0, p.dh_vec, dx);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float xh = (h[i][e] * k) * rk;
-        dw[i][e] = __builtin_fmaf(g[i][e], xh, dw[i][e]);
-        dx[e] = __builtin_fmaf(r, __builtin_fmaf(-xh, mean, g[i][e] * w[i][e]), dx[e]);
+        const float xh = (x[i][e] * k) * rk;
+        dw[i][e] = __builtin_fmaf(dy[i][e], xh, dw[i][e]);
+        dx[e] = __builtin_fmaf(r, __builtin_fmaf(-xh, mean, dy[i][e] * w[i][e]), dx[e]);
       }
       store8(p.dx, p.dx_bf16, ox, at, p.H, p.dx_vec, dx);
     }
@@ -192,6 +209,7 @@ __global__ __launch_bounds__(1024) void rms_norm_bwd_weight_kernel(const float* 
   float s = 0.0f;
   if (c < H) {
     const int end = min(parts, (run + 1) * per);
+#pragma unroll 8
     for (int i = run * per; i < end; ++i) s += part[(int64_t)i * H + c];
   }
   sums[run][threadIdx.x & 31] = s;

@@ -7,7 +7,8 @@
 //   gradient, with z = dy w:
 //   dg = z u s (1 + g (1 - s)),  du = z g s,  dw = sum over the row of dy (g s) u
 //
-// Sixteen lanes take a 128-element block of a row, eight elements each.
+// A row takes 16 to 256 lanes, eight elements each and two such chunks at a time; 16
+// lanes hold a 128-element block of the cast.
 
 #include <type_traits>
 
@@ -34,28 +35,43 @@ __device__ __forceinline__ int live_rows(const int32_t* masked, int g, int rows)
   return masked == nullptr ? rows : min(max(masked[g], 0), rows);
 }
 
+// Lanes of a row of I: 16 hold a block, two chunks of 8 elements a lane where there are enough.
+constexpr int fwd_lanes(int64_t I) { return I <= 128 ? 16 : I <= 512 ? 32 : I <= 1024 ? 64 : I <= 2048 ? 128 : 256; }
+
+template <int NT>
 __global__ __launch_bounds__(256) void swiglu_kernel(const SwigluArgs p) {
-  const int sub = threadIdx.x & 15;
-  const int64_t unit = (int64_t)blockIdx.x * 16 + (threadIdx.x >> 4);  // a block of a row
-  const int blk = (int)(unit % p.blocks);
-  const int64_t row = unit / p.blocks;
-  const int g = (int)(row / p.R), r = (int)(row % p.R);
-  if (g >= p.G || r >= live_rows(p.masked, g, p.R)) return;  // (whole groups of 16 lanes)
-  const int at = blk * 128 + sub * 8;
-  const int64_t ox = g * p.sx_g + r * p.sx_r;
-  float a[8], b[8];
-  load8(p.x, p.x_bf16, ox, at, p.I, p.x_vec, a);
-  load8(p.x, p.x_bf16, ox + p.I, at, p.I, p.u_vec, b);
+  constexpr int NI = NT == 16 ? 1 : 2;
+  const int lane = threadIdx.x % NT;
+  const uint32_t row = blockIdx.x * (256 / NT) + threadIdx.x / NT;
+  if (row >= (uint32_t)(p.G * p.R)) return;  // (whole rows, as below)
+  const int g = p.G == 1 ? 0 : (int)(row / (uint32_t)p.R), r = (int)(row - (uint32_t)g * p.R);
+  if (r >= live_rows(p.masked, g, p.R)) return;
+  const int64_t ox = g * p.sx_g + r * p.sx_r, oy = g * p.sy_g + r * p.sy_r;
+  uint8_t* q = p.q + g * p.sq_g + r * p.sq_r;
+  float* sf = p.sf + g * p.ss_g + r * p.ss_r;
   const float w = p.w != nullptr ? p.w[row * p.sw] : 1.0f;
+  for (int from = 0; from < p.I; from += NT * NI * 8) {
+    float a[NI][8], b[NI][8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) a[e] = (a[e] * sigmoid(a[e])) * b[e] * w;
-  if (p.y != nullptr) store8(p.y, p.y_bf16, g * p.sy_g + r * p.sy_r, at, p.I, p.y_vec, a);
-  if (p.q == nullptr) return;
-  uint32_t lo, hi;
-  const float s = cast_block8(a, p.ue8m0, lo, hi);
-  if (at >= p.I) return;
-  store_codes8(p.q + g * p.sq_g + r * p.sq_r, at, p.I, p.q_vec, lo, hi);
-  if (sub == 0) p.sf[g * p.ss_g + r * p.ss_r + blk * p.ss_k] = s;
+    for (int i = 0; i < NI; ++i) {
+      const int at = from + (lane + i * NT) * 8;
+      load8(p.x, p.x_bf16, ox, at, p.I, p.x_vec, a[i]);
+      load8(p.x, p.x_bf16, ox + p.I, at, p.I, p.u_vec, b[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+      const int at = from + (lane + i * NT) * 8;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) a[i][e] = (a[i][e] * sigmoid(a[i][e])) * b[i][e] * w;
+      if (p.y != nullptr) store8(p.y, p.y_bf16, oy, at, p.I, p.y_vec, a[i]);
+      if (p.q == nullptr) continue;
+      uint32_t lo, hi;
+      const float s = cast_block8(a[i], p.ue8m0, lo, hi);
+      if (at >= p.I) continue;
+      store_codes8(q, at, p.I, p.q_vec, lo, hi);
+      if ((lane & 15) == 0) sf[(at >> 7) * p.ss_k] = s;
+    }
+  }
 }
 
 // One row takes NT lanes.
@@ -63,9 +79,10 @@ template <int NT>
 __global__ __launch_bounds__(256) void swiglu_bwd_kernel(const SwigluBwdArgs p) {
   __shared__ float red[4];
   const int lane = threadIdx.x % NT;
-  const int64_t row = (int64_t)blockIdx.x * (256 / NT) + threadIdx.x / NT;
-  const int g = (int)(row / p.R), r = (int)(row % p.R);
-  if (g >= p.G || r >= live_rows(p.masked, g, p.R)) return;
+  const uint32_t row = blockIdx.x * (256 / NT) + threadIdx.x / NT;
+  if (row >= (uint32_t)(p.G * p.R)) return;
+  const int g = p.G == 1 ? 0 : (int)(row / (uint32_t)p.R), r = (int)(row - (uint32_t)g * p.R);
+  if (r >= live_rows(p.masked, g, p.R)) return;
   const int64_t ox = g * p.sx_g + r * p.sx_r, oy = g * p.sy_g + r * p.sy_r, od = g * p.sd_g + r * p.sd_r;
   const float w = p.w != nullptr ? p.w[row * p.sw] : 1.0f;
   float sum = 0.0f;
@@ -92,15 +109,21 @@ __global__ __launch_bounds__(256) void swiglu_bwd_kernel(const SwigluBwdArgs p) 
 
 }  // namespace
 
-int64_t swiglu_grid(int64_t rows, int64_t I) { return (rows * ((I + 127) / 128) + 15) / 16; }
+int64_t swiglu_grid(int64_t rows, int64_t I) { return (rows * fwd_lanes(I) + 255) / 256; }
 int64_t swiglu_bwd_grid(int64_t rows, int64_t I) {
   const int64_t per = I <= 128 ? 16 : I <= 512 ? 4 : 1;
   return (rows + per - 1) / per;
 }
 
-hipError_t launch_swiglu(SwigluArgs p, hipStream_t stream) {
-  p.blocks = (p.I + 127) / 128;
-  swiglu_kernel<<<dim3((unsigned)swiglu_grid((int64_t)p.G * p.R, p.I)), dim3(256), 0, stream>>>(p);
+hipError_t launch_swiglu(const SwigluArgs& p, hipStream_t stream) {
+  const dim3 grid((unsigned)swiglu_grid((int64_t)p.G * p.R, p.I)), block(256);
+  switch (fwd_lanes(p.I)) {
+    case 16: swiglu_kernel<16><<<grid, block, 0, stream>>>(p); break;
+    case 32: swiglu_kernel<32><<<grid, block, 0, stream>>>(p); break;
+    case 64: swiglu_kernel<64><<<grid, block, 0, stream>>>(p); break;
+    case 128: swiglu_kernel<128><<<grid, block, 0, stream>>>(p); break;
+    default: swiglu_kernel<256><<<grid, block, 0, stream>>>(p); break;
+  }
   return hipGetLastError();
 }
 
