@@ -4,16 +4,16 @@
 
 Every matrix product, cast, cache and routing step is a call of this library:
 
-    x -> norm -> q, k, v projection (per-token cast + FP8 GEMM)
+    x -> rms_norm, cast to FP8 -> q, k, v projection (FP8 GEMM)
       -> kv_append_fp8: keys rotated into the paged cache, queries rotated
       -> paged_attention_fp8 over the cache -> output projection
-      -> norm -> router logits (BF16 GEMM, FP32 out) -> moe_route_topk
+      -> rms_norm with the residual's addition -> router logits (BF16 GEMM, FP32
+         out) -> moe_route_topk
       -> moe_dispatch_masked_fp8 -> gate / up GEMM of every expert
-      -> silu(gate) * up -> per-token cast -> down GEMM -> moe_combine
+      -> swiglu, cast to FP8 -> down GEMM -> moe_combine
 
-The norms, the activation and the residual additions are plain torch.  Weights
-are random; the prompt goes through the same calls as a decode step, with as
-many queries a sequence as it has tokens.  The decode step is captured into a
+Weights are random (those of the norms one); the prompt goes through the same
+calls as a decode step, with as many queries a sequence as it has tokens.  The decode step is captured into a
 hipGraph once and replayed.
 """
 
@@ -39,10 +39,6 @@ def _quantized(shape, gen, gain=1.0):
     return q, sf
 
 
-def _norm(x):
-    return x * torch.rsqrt(x.float().square().mean(dim=-1, keepdim=True) + 1e-6).to(x.dtype)
-
-
 class DecodeLayer:
     """Weights, the paged cache of `batch` sequences of up to max_tokens, and the layer's forward."""
 
@@ -52,6 +48,7 @@ class DecodeLayer:
         gen.manual_seed(seed)
         self.batch, self.hidden, self.heads, self.kv_heads, self.head_dim = batch, hidden, heads, kv_heads, head_dim
         self.experts, self.choices, self.inter = experts, choices, inter
+        self.w_norm = torch.ones(2, hidden, dtype=torch.bfloat16, device="cuda")
         self.w_qkv = _quantized(((heads + 2 * kv_heads) * head_dim, hidden), gen)
         self.w_out = _quantized((hidden, heads * head_dim), gen)
         self.w_router = (torch.randn(experts, hidden, generator=gen, device="cuda") / hidden ** 0.5).to(torch.bfloat16)
@@ -71,19 +68,22 @@ class DecodeLayer:
         self.cos_sin = torch.cat([ang.cos(), ang.sin()], dim=1).float()
         self.routes = None  # the last step's (topk_idx, topk_weights)
 
-    def _linear(self, x, weight):
-        """x [M, K] BF16 times an FP8 weight [N, K], BF16 out."""
-        (M, K), (w, sfw) = x.shape, weight
-        a = torch.empty(M, K, dtype=torch.uint8, device="cuda")
-        sfa = torch.empty(K // 128, M, device="cuda").t()
-        d = torch.empty(M, w.shape[0], dtype=torch.bfloat16, device="cuda")
-        mg.per_token_cast_to_fp8(x, a, sfa)
+    def _codes(self, M, K):
+        """Room for FP8 rows and their scales."""
+        return torch.empty(M, K, dtype=torch.uint8, device="cuda"), torch.empty(K // 128, M, device="cuda").t()
+
+    def _linear(self, codes, weight):
+        """FP8 rows [M, K] times an FP8 weight [N, K], BF16 out."""
+        (a, sfa), (w, sfw) = codes, weight
+        d = torch.empty(a.shape[0], w.shape[0], dtype=torch.bfloat16, device="cuda")
         return mg.fp8_gemm_nt(a, w, sfa, sfw, None, d)
 
     def attention(self, x, n):
         """x [batch * n, hidden]: n new tokens of every sequence."""
         S, H, G, D = self.batch, self.heads, self.kv_heads, self.head_dim
-        qkv = self._linear(x, self.w_qkv).view(S * n, H + 2 * G, D)
+        codes = self._codes(*x.shape)
+        mg.rms_norm(x, self.w_norm[0], q=codes[0], sf=codes[1])
+        qkv = self._linear(codes, self.w_qkv).view(S * n, H + 2 * G, D)
         q = torch.empty(S * n, H, D, dtype=torch.bfloat16, device="cuda")
         cu = torch.arange(0, S * n + 1, n, dtype=torch.int32, device="cuda")
         mg.kv_append_fp8(qkv[:, H:H + G], qkv[:, H + G:], *self.cache, self.table, cu, self.lens, cos_sin=self.cos_sin,
@@ -93,7 +93,9 @@ class DecodeLayer:
         need = mg.paged_attention_fp8_workspace(S, n, H, G, D, self.max_tokens)
         mg.paged_attention_fp8(q.view(S, n, H, D), *self.cache, self.table, self.lens, out, D ** -0.5,
                                workspace=torch.empty(-(-need // 4), device="cuda"))
-        return self._linear(out.view(S * n, H * D), self.w_out)
+        codes = self._codes(S * n, H * D)
+        mg.per_token_cast_to_fp8(out.view(S * n, H * D), *codes)
+        return self._linear(codes, self.w_out)
 
     def moe(self, x):
         T, E, k, I = x.shape[0], self.experts, self.choices, self.inter
@@ -112,10 +114,9 @@ class DecodeLayer:
         mg.moe_dispatch_masked_fp8(x, idx, a, sfa, rows, slot, src)
         up = torch.empty(E, T, 2 * I, dtype=torch.bfloat16, device="cuda")
         mg.m_grouped_fp8_gemm_nt_masked(a, self.w_up[0], sfa, self.w_up[1], up, rows, T)
-        act = torch.nn.functional.silu(up[..., :I]) * up[..., I:]
         b = torch.empty(E, T, I, dtype=torch.uint8, device="cuda")
         sfb = torch.empty(E, T, I // 128, device="cuda")
-        mg.per_token_cast_to_fp8(act, b, sfb)
+        mg.swiglu(up, q=b, sf=sfb, masked_m=rows)
         down = torch.empty(E, T, self.hidden, dtype=torch.bfloat16, device="cuda")
         mg.m_grouped_fp8_gemm_nt_masked(b, self.w_down[0], sfb, self.w_down[1], down, rows, T)
         return mg.moe_combine(down, slot, weights, torch.empty_like(x))
@@ -124,9 +125,9 @@ class DecodeLayer:
         """x BF16 [batch, n, hidden]: n new tokens of every sequence -> the layer's output for them."""
         S, n, C = x.shape
         x = x.reshape(S * n, C)
-        x = x + self.attention(_norm(x), n)
-        x = x + self.moe(_norm(x))
-        return x.view(S, n, C)
+        h, y = torch.empty_like(x), torch.empty_like(x)
+        mg.rms_norm(self.attention(x, n), self.w_norm[1], y=y, residual=x, h=h)
+        return (h + self.moe(y)).view(S, n, C)
 
 
 def main():
