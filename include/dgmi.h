@@ -517,7 +517,9 @@ int64_t paged_attention_fp8_workspace(int64_t S, int64_t n, int64_t Hq, int64_t 
  * FP8 in the same kernel (the operand of the FP8 GEMMs):
  *   h = x + residual, y = h / sqrt(mean(h^2) + eps) * weight
  *   x         F32 or BF16 [T, H], or [T, heads, H] (each head of a projection's
- *             output), any strides of the outer dims (innermost 1); H <= 16384
+ *             output), any strides of the outer dims (innermost 1); H <= 16384,
+ *             at most 2^22 - 1 rows (2^24 - 4 up to H = 2048, 2^26 - 16 up to
+ *             1024, 2^28 - 64 up to 128)
  *   weight    F32 or BF16 [H]
  *   residual  NULL, or F32 or BF16 of x's shape
  *   h         NULL, or of the residual's type and x's shape, out: the sum,
@@ -531,7 +533,7 @@ int64_t paged_attention_fp8_workspace(int64_t S, int64_t n, int64_t Hq, int64_t 
  *   eps       positive and finite
  * One of y and q is wanted.  h and y may take the place of x or the residual
  * (same base, type and strides); any other overlap is rejected.  Rows whose
- * squares leave FP32's range are computed as those of smaller ones.
+ * squares leave FP32's range, at either end, are computed as others are.
  */
 int rms_norm(const dg_tensor* x, const dg_tensor* weight, const dg_tensor* y, const dg_tensor* q, const dg_tensor* sf,
              const dg_tensor* residual, const dg_tensor* h, float eps, int use_ue8m0, hipStream_t stream);
@@ -600,8 +602,9 @@ int swiglu_bwd(const dg_tensor* x, const dg_tensor* grad_y, const dg_tensor* gra
  *   tn  d[g] = c[g] + a_g^T . b_g     a [M, N], b [M, K], d [G, N, K]: the
  *       gradient of nt's b, the contraction over the group's rows; an empty
  *       group gives c[g], or zeros
- *   a, b     BF16, row and group strides multiples of 8 elements, 16-byte
- *            aligned bases; any M, N and (tn) K, K of nt and nn a multiple of 64
+ *   a, b     BF16, row and group strides multiples of 8 elements, rows that do
+ *            not overlap, 16-byte aligned bases; any M, N and (tn) K, K of nt and
+ *            nn a multiple of 64
  *   c        NULL, or BF16 or F32 of d's shape; it may be d itself (same base,
  *            type and strides), any other overlap is rejected
  *   d        BF16 or F32, any row stride (innermost 1).  Rows of nt and nn

@@ -1521,8 +1521,6 @@ int check_fp8_out(const dg_tensor* q, const dg_tensor* sf, const dg_tensor* x, i
   return DG_OK;
 }
 constexpr int64_t kMaxNormRow = 16384;
-// Workgroups of up to 1024 threads.
-constexpr int64_t kMaxGroups1024 = (int64_t(1) << 22) - 1;
 
 }  // namespace
 
@@ -1556,7 +1554,9 @@ int rms_norm(const dg_tensor* x, const dg_tensor* weight, const dg_tensor* y, co
   DG_TRY(check_fp8_out(q, sf, x, H, fname));
   if (!(eps > 0.0f && eps - eps == 0.0f)) return fail(DG_INVALID_ARG, "%s: eps must be positive and finite", fname);
   if (H > kMaxNormRow) return fail(DG_UNSUPPORTED, "%s: rows of at most %lld elements (got %lld)", fname, (long long)kMaxNormRow, (long long)H);
-  if (rows > kMaxGroups1024) return fail(DG_UNSUPPORTED, "%s: at most 2^22 - 1 rows a call (got %lld)", fname, (long long)rows);
+  if (rows > dgmi::rms_norm_max_rows(H))
+    return fail(DG_UNSUPPORTED, "%s: at most %lld rows of %lld elements a call (got %lld)", fname,
+                (long long)dgmi::rms_norm_max_rows(H), (long long)H, (long long)rows);
   const dg_tensor* outs[] = {h, y, q, sf};
   const char* onames[] = {"h", "y", "q", "sf"};
   const dg_tensor* ins[] = {x, residual, weight};
@@ -1619,7 +1619,7 @@ int rms_norm(const dg_tensor* x, const dg_tensor* weight, const dg_tensor* y, co
 }
 
 int64_t rms_norm_bwd_workspace(int64_t rows, int64_t H) {
-  if (rows <= 0 || rows > kMaxGroups1024 || H <= 0 || H > kMaxNormRow) return 0;
+  if (rows <= 0 || H <= 0 || H > kMaxNormRow || rows > dgmi::rms_norm_max_rows(H)) return 0;
   return dgmi::rms_norm_bwd_parts(rows, H) * H * 4;
 }
 
@@ -1647,7 +1647,9 @@ int rms_norm_bwd(const dg_tensor* grad_y, const dg_tensor* h, const dg_tensor* w
   }
   if (!(eps > 0.0f && eps - eps == 0.0f)) return fail(DG_INVALID_ARG, "%s: eps must be positive and finite", fname);
   if (H > kMaxNormRow) return fail(DG_UNSUPPORTED, "%s: rows of at most %lld elements (got %lld)", fname, (long long)kMaxNormRow, (long long)H);
-  if (rows > kMaxGroups1024) return fail(DG_UNSUPPORTED, "%s: at most 2^22 - 1 rows a call (got %lld)", fname, (long long)rows);
+  if (rows > dgmi::rms_norm_max_rows(H))
+    return fail(DG_UNSUPPORTED, "%s: at most %lld rows of %lld elements a call (got %lld)", fname,
+                (long long)dgmi::rms_norm_max_rows(H), (long long)H, (long long)rows);
   DG_TRY(check_rows_apart(grad_x, "grad_x"));
   const int64_t need = grad_weight != nullptr ? rms_norm_bwd_workspace(rows, H) : 0;
   if (need > 0) {
@@ -1882,6 +1884,15 @@ int swiglu_bwd(const dg_tensor* x, const dg_tensor* grad_y, const dg_tensor* gra
 
 namespace {
 
+// Row stride of an operand of the ragged products, whose loads take a row to end before the next begins; of a single
+// row, whose stride may be anything, its length.
+int operand_stride(const dg_tensor* t, const char* name, int64_t* ld, const char* fname) {
+  const int64_t rows = t->shape[t->ndim - 2], n = t->shape[t->ndim - 1];
+  *ld = rows > 1 ? row_stride(t) : (n + 7) / 8 * 8;
+  if (rows > 1 && n > 0 && *ld < n) return fail(DG_INVALID_ARG, "%s: rows of %s overlap in memory", fname, name);
+  return DG_OK;
+}
+
 // The ragged products.  nt: a [M, K], b [G, N, K], d [M, N]; nn: a [M, K], b [G, K, N],
 // d [M, N]; tn: a [M, N], b [M, K], d [G, N, K].
 int ragged_common(int layout, const dg_tensor* a, const dg_tensor* b, const dg_tensor* c, const dg_tensor* d,
@@ -1910,7 +1921,10 @@ int ragged_common(int layout, const dg_tensor* a, const dg_tensor* b, const dg_t
   if (!tn && K % 64 != 0) return fail(DG_UNSUPPORTED, "%s: K = %lld is not a multiple of 64", fname, (long long)K);
   for (const dg_tensor* t : {a, b})
     if (!rows_on(t, 16)) return fail(DG_INVALID_ARG, "%s: a and b need 16-byte aligned bases and row/group strides", fname);
-  DG_TRY(check_row_strides(2 * row_stride(a), 2 * row_stride(b), fname));
+  int64_t lda = 0, ldb = 0;
+  DG_TRY(operand_stride(a, "a", &lda, fname));
+  DG_TRY(operand_stride(b, "b", &ldb, fname));
+  DG_TRY(check_row_strides(2 * lda, 2 * ldb, fname));
   if (!aligned(d->data, elem_size(d->dtype))) return fail(DG_INVALID_ARG, "%s: d must be element-aligned", fname);
   DG_TRY(check_rows_apart(d, "d"));
   if (c != nullptr) {
@@ -1926,7 +1940,7 @@ int ragged_common(int layout, const dg_tensor* a, const dg_tensor* b, const dg_t
   DG_TRY(check_no_alias(d, "d", b, "b"));
   DG_TRY(check_no_alias(d, "d", offsets, "offsets"));
   if (G == 0 || N == 0 || (tn ? K : M) == 0) return ok();
-  if (dgmi::ragged_tiles(layout, G, M, N, K) > INT32_MAX - 4096)
+  if (dgmi::ragged_tiles(layout, G, M, N, K) > (double)(INT32_MAX - 4096))
     return fail(DG_UNSUPPORTED, "%s: too many groups, rows and columns for one call", fname);
   dgmi::RaggedArgs p = {};
   p.a = static_cast<const uint16_t*>(a->data);
@@ -1934,8 +1948,8 @@ int ragged_common(int layout, const dg_tensor* a, const dg_tensor* b, const dg_t
   p.d = d->data;
   p.c = c != nullptr ? c->data : nullptr;
   p.offsets = static_cast<const int32_t*>(offsets->data);
-  p.lda = a->stride[0];
-  p.ldb = row_stride(b);
+  p.lda = lda;
+  p.ldb = ldb;
   p.b_gs = group_stride(b);
   p.ldd = row_stride(d);
   p.d_gs = group_stride(d);

@@ -274,6 +274,7 @@ int64_t paged_attention_workspace(int64_t S, int64_t n, int64_t Hq, int64_t Hkv,
 // largest grid of the call's kernels
 int64_t paged_attention_grid(int64_t S, int64_t Hkv, int64_t row_tiles, int64_t D, int64_t cap);
 hipError_t launch_paged_attention(PagedAttnArgs p, hipStream_t stream);
+int64_t rms_norm_max_rows(int64_t H);
 int64_t rms_norm_bwd_parts(int64_t rows, int64_t H);
 hipError_t launch_rms_norm(const RmsNormArgs& p, hipStream_t stream);
 hipError_t launch_rms_norm_bwd(const RmsNormBwdArgs& p, hipStream_t stream);
@@ -282,7 +283,7 @@ int64_t swiglu_bwd_grid(int64_t rows, int64_t I);
 hipError_t launch_swiglu(const SwigluArgs& p, hipStream_t stream);
 hipError_t launch_swiglu_bwd(const SwigluBwdArgs& p, hipStream_t stream);
 // tiles of a call at most (a kernel counts them in 31 bits)
-int64_t ragged_tiles(int layout, int64_t G, int64_t M, int64_t N, int64_t K);
+double ragged_tiles(int layout, int64_t G, int64_t M, int64_t N, int64_t K);
 hipError_t launch_ragged(RaggedArgs p, int layout, hipStream_t stream);
 hipError_t launch_per_block(const QuantArgs& p, hipStream_t stream);
 hipError_t launch_pack_ue8m0(const PackArgs& p, hipStream_t stream);

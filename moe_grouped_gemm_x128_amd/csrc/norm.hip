@@ -11,8 +11,16 @@
 //
 // A row is held in registers by NT lanes, NI chunks of 8 elements each, chunk c
 // of the row in lane c % NT: 16 lanes hold one 128-element block of the cast,
-// whose maximum is reduced without shared memory.  Squares that leave FP32's
-// range (rows of values past 2^60) are taken again of h 2^-64.
+// whose maximum is reduced without shared memory.  Where squares leave FP32's
+// range (their sum past it, or below 2^-100 with an eps there too) they are taken
+// again of h 2^-64 or h 2^96.
+//
+// What bounds it: memory.  Read once, written once: 16384 rows of 7168 with the
+// residual, its sum and FP8 codes (826 MB) take 161 us, 5.1 TB/s; 65536 x 1024
+// without them 41 us, 6.6 TB/s from the last cache.  The gradient holds the row, its
+// gradient, the weight and the weight's sums, so that 4 waves of 512-lane rows fit a
+// SIMD, and waits for a row's sums before it stores: 8192 x 4096 38 us (5.3 TB/s),
+// 8192 x 7168 96 us (3.7 TB/s); the weight's gradient adds 7 to 11 us.
 
 #include <type_traits>
 
@@ -23,7 +31,10 @@ namespace dgmi {
 
 namespace {
 
-constexpr float TINY = 0x1p-64f;  // factor of rows whose squares overflow
+// The sum of squares s of a row has left FP32's range, or lost bits that eps does not cover: the row is taken again
+// with this factor on its values.
+__device__ __forceinline__ bool out_of_range(float s, float eps) { return !(s < INFINITY) || (s < 0x1p-100f && eps < 0x1p-100f); }
+__device__ __forceinline__ float factor_of(float s) { return s < 0x1p-100f ? 0x1p96f : 0x1p-64f; }
 
 template <int NT>
 constexpr int rows_of() { return NT < 256 ? 256 / NT : 1; }  // rows a workgroup takes side by side
@@ -66,13 +77,13 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(const Rms
     for (int e = 0; e < 8; ++e) s = __builtin_fmaf(v[i][e], v[i][e], s);
   s = row_sum<NT>(s, red);
   float k = 1.0f;
-  if (!(s < INFINITY)) {  // (the whole row takes this turn)
-    k = TINY;
+  if (out_of_range(s, p.eps)) {  // (the whole row takes this turn)
+    k = factor_of(s);
     s = 0.0f;
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) s += (v[i][e] * TINY) * (v[i][e] * TINY);
+      for (int e = 0; e < 8; ++e) s += (v[i][e] * k) * (v[i][e] * k);
     s = row_sum<NT>(s, red);
   }
   const float r = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(s, (float)p.H) + p.eps * k * k));
@@ -97,7 +108,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(const Rms
 // Rows blockIdx, + gridDim, ... of the gradient; the weight's sums stay in
 // registers and leave as one row of partial sums a workgroup.
 template <int NT, int NI>
-__global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_bwd_kernel(const RmsNormBwdArgs p) {
+__global__ __launch_bounds__(NT < 256 ? 256 : NT, NT == 512 ? 4 : 1) void rms_norm_bwd_kernel(const RmsNormBwdArgs p) {
   constexpr int RW = rows_of<NT>();
   __shared__ float red[NT / 64 + 1];
   __shared__ float sums[2][2][NT / 64 + 1];
@@ -146,15 +157,15 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_bwd_kernel(const
       }
     }
     float k = 1.0f;
-    if (!(s < INFINITY)) {  // (the whole row takes this turn)
-      k = TINY;
+    if (out_of_range(s, p.eps)) {  // (the whole row takes this turn)
+      k = factor_of(s);
       s = m = 0.0f;
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          s += (x[i][e] * TINY) * (x[i][e] * TINY);
-          m += dy[i][e] * w[i][e] * (x[i][e] * TINY);
+          s += (x[i][e] * k) * (x[i][e] * k);
+          m += dy[i][e] * w[i][e] * (x[i][e] * k);
         }
       s = row_sum<NT>(s, red);
       m = row_sum<NT>(m, red);
@@ -222,8 +233,11 @@ __global__ __launch_bounds__(1024) void rms_norm_bwd_weight_kernel(const float* 
   }
 }
 
-// Lanes and chunks that hold a row of H: NT * NI * 8 >= H.
-template <class F>
+// Lanes and chunks that hold a row of H: NT * NI * 8 >= H.  Forward: two chunks a lane past 2048 (16384 rows of 4096
+// with residual and codes 89 us, 512 lanes of one chunk 108), 512 lanes past 4096 (8192 x 7168 84 us, 256 lanes of
+// four chunks 95, 1024 of one 125).  The gradient has more to hold a chunk: one up to 4096 (16384 x 4096 97 us, 256
+// lanes of two 161), two past it (8192 x 7168 107 us, 1024 lanes of one 111).
+template <bool BWD, class F>
 hipError_t with_row_shape(int64_t H, F f) {
 #define DGMI_ROW(NT_, NI_) \
   if (H <= (int64_t)NT_ * NI_ * 8) return f(std::integral_constant<int, NT_>{}, std::integral_constant<int, NI_>{})
@@ -232,7 +246,8 @@ hipError_t with_row_shape(int64_t H, F f) {
   DGMI_ROW(64, 1);
   DGMI_ROW(64, 2);
   DGMI_ROW(256, 1);
-  DGMI_ROW(512, 1);
+  if constexpr (BWD) DGMI_ROW(512, 1);
+  else DGMI_ROW(256, 2);
   DGMI_ROW(512, 2);
   DGMI_ROW(1024, 2);
 #undef DGMI_ROW
@@ -241,15 +256,27 @@ hipError_t with_row_shape(int64_t H, F f) {
 
 }  // namespace
 
-// Partial rows of the weight's gradient: workgroups of the gradient kernel.
+// Rows of H that one launch takes: 2^32 threads less than a workgroup.
+int64_t rms_norm_max_rows(int64_t H) {
+  int64_t lanes = 1024;
+  (void)with_row_shape<true>(H, [&](auto nt, auto) {
+    lanes = decltype(nt)::value;
+    return hipSuccess;
+  });
+  return ((int64_t(1) << 32) - 1024) / lanes;
+}
+
+// Partial rows of the weight's gradient: workgroups of the gradient kernel.  Of 256 lanes four to a compute unit (32768
+// x 2048 94 us, two 147, three 108, eight 98), of 512 lanes two (8191 x 4096 62 us, three 71, four 67).
 int64_t rms_norm_bwd_parts(int64_t rows, int64_t H) {
   const int64_t per = H <= 128 ? 16 : H <= 256 ? 8 : H <= 1024 ? 4 : 1;  // rows a workgroup takes side by side
   const int64_t groups = (rows + per - 1) / per;
-  return groups < 512 ? groups : 512;
+  const int64_t most = H <= 2048 ? 1024 : 512;
+  return groups < most ? groups : most;
 }
 
 hipError_t launch_rms_norm(const RmsNormArgs& p, hipStream_t stream) {
-  return with_row_shape(p.H, [&](auto nt, auto ni) {
+  return with_row_shape<false>(p.H, [&](auto nt, auto ni) {
     constexpr int NT = decltype(nt)::value, NI = decltype(ni)::value;
     const int64_t blocks = (p.rows + rows_of<NT>() - 1) / rows_of<NT>();
     rms_norm_kernel<NT, NI><<<dim3((unsigned)blocks), dim3(NT < 256 ? 256 : NT), 0, stream>>>(p);
@@ -259,7 +286,7 @@ hipError_t launch_rms_norm(const RmsNormArgs& p, hipStream_t stream) {
 
 hipError_t launch_rms_norm_bwd(const RmsNormBwdArgs& p, hipStream_t stream) {
   const int64_t parts = rms_norm_bwd_parts(p.rows, p.H);
-  const hipError_t e = parts == 0 ? hipSuccess : with_row_shape(p.H, [&](auto nt, auto ni) {
+  const hipError_t e = parts == 0 ? hipSuccess : with_row_shape<true>(p.H, [&](auto nt, auto ni) {
     constexpr int NT = decltype(nt)::value, NI = decltype(ni)::value;
     rms_norm_bwd_kernel<NT, NI><<<dim3((unsigned)parts), dim3(NT < 256 ? 256 : NT), 0, stream>>>(p);
     return hipGetLastError();

@@ -109,7 +109,7 @@ struct Tile {
 };
 
 template <class T, int LAY, bool F32>
-__global__ __launch_bounds__(T::NT) void ragged_kernel(const RaggedArgs p) {
+__global__ __launch_bounds__(T::NT, 2) void ragged_kernel(const RaggedArgs p) {
   constexpr bool A_MN = LAY == RAGGED_TN, B_MN = LAY != RAGGED_NT;
   constexpr int S = T::STAGES;
   static_assert(S == 2 || S == 3, "two or three stages");
@@ -645,9 +645,9 @@ hipError_t launch_shape(RaggedArgs p, int layout, hipStream_t stream) {
 }  // namespace
 
 // Tiles that a call may have to count: with offsets that fall each group may hold all rows.
-int64_t ragged_tiles(int layout, int64_t G, int64_t M, int64_t N, int64_t K) {
-  if (layout == RAGGED_TN) return G * tiles(N, Mid::BM) * tiles(K, Mid::BN);
-  return G * (M / Few::BM + 1) * tiles(N, Few::BN);
+double ragged_tiles(int layout, int64_t G, int64_t M, int64_t N, int64_t K) {
+  if (layout == RAGGED_TN) return (double)G * (double)tiles(N, Mid::BM) * (double)tiles(K, Mid::BN);
+  return (double)G * (double)(M / Few::BM + 1) * (double)tiles(N, Few::BN);
 }
 
 // Slice times in those of Big, from sweeps of 4 to 8192 rows in 1 to 64 groups

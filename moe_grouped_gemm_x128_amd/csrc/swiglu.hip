@@ -40,8 +40,9 @@ __device__ __forceinline__ int live_rows(const int32_t* masked, int g, int rows)
   return masked == nullptr ? rows : min(max(masked[g], 0), rows);
 }
 
-// Lanes of a row of I, eight elements each at a time (two chunks a lane: 6144 rows of 2048 18.5 us for 16.0).
-constexpr int fwd_lanes(int64_t I) { return I <= 128 ? 16 : I <= 512 ? 32 : I <= 512 ? 64 : I <= 1024 ? 128 : 256; }
+// Lanes of a row of I, eight elements each at a time: as many as one chunk a lane takes (two chunks a lane: 6144 rows
+// of 2048 18.5 us for 16.0, 32768 of 512 17.8 for 16.8; half of the lanes idle: 16384 rows of 1024 27.1 for 16.4).
+constexpr int fwd_lanes(int64_t I) { return I <= 128 ? 16 : I <= 256 ? 32 : I <= 512 ? 64 : I <= 1024 ? 128 : 256; }
 
 template <int NT>
 __global__ __launch_bounds__(256) void swiglu_kernel(const SwigluArgs p) {

@@ -70,8 +70,8 @@ def test_norm_refusals():
     for eps in (0.0, -1e-6, float("nan"), float("inf")):
         _refused(n, INVALID, x, w, y=y, eps=eps)
     _refused(n, UNSUPPORTED, _t((1, 16392), BF16), _t(16392), y=_t((1, 16392), BF16))
-    many = _t((1, 8), BF16).expand(2 ** 22, 8)
-    _refused(n, UNSUPPORTED, many, _t(8), y=_t((2 ** 22, 8), BF16))
+    _refused(n, UNSUPPORTED, _t((1, 1), BF16).expand(2 ** 28, 1), _t(1), y=torch.empty((2 ** 28, 1), dtype=BF16))
+    _taken(n, _t((1, 8), BF16).expand(2 ** 22, 8), _t(8), y=torch.empty((2 ** 22, 8), dtype=BF16))
     # in place over x or the residual as they are, and nothing else
     _taken(n, x, w, y=x)
     r = _t((T, H), BF16)
@@ -191,6 +191,9 @@ def test_ragged_refusals(form):
     wide = _t(sd[:-1] + (sd[-1] + 8,), BF16)
     assert "overlaps" in no(INVALID, d=wide[..., :sd[-1]], c=wide[..., 8:])
     no(INVALID, d=d[:1].expand(sd))
+    assert "overlap" in no(INVALID, a=a[:1].expand(sa))
+    assert "overlap" in no(INVALID, b=b[..., :1, :].expand(sb))
+    assert "overlap" in no(INVALID, a=a.view(-1)[:8 * sa[0] + sa[1]].as_strided(sa, (8, 1)))
     no(UNSUPPORTED, a=_far(sa))
     if form != "tn":
         no(UNSUPPORTED, a=_t((M, 96), BF16), b=_t((G, N, 96) if form == "nt" else (G, 96, N), BF16))

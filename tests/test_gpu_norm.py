@@ -171,6 +171,48 @@ def test_rows_at_the_edges_of_fp32():
     _close(dw, rw, 130 * U * wsize + 1e-37, "grad_weight")
 
 
+@pytest.mark.parametrize("H", [100, 300, 4096])
+def test_an_eps_below_the_squares_range(H):
+    """Squares that FP32 cannot hold count where eps does not cover them."""
+    say(f"rms_norm of small rows with a small eps, H={H}")
+    gen = _gen(11)
+    x = torch.randn(6, H, generator=gen, device="cuda", dtype=torch.float64)
+    for i, f in enumerate((1.0, 1e-14, 1e-16, 1e-20, 1e-25, 1e-36)):
+        x[i] *= f
+    x, w, dy = x.float(), _rows(gen, (H,), F32), _rows(gen, (6, H), F32, 1e-6)
+    for eps in (1e-28, 1e-32, 1e-38, float(np.float32(1e-44))):
+        y = _blank((6, H), F32)
+        mg.rms_norm(x, w, y=y, eps=eps)
+        want = layer.rms_norm(_np(x), _np(w), float(np.float32(eps)))
+        _close(y, want, 26 * U * np.abs(want) + 1e-37, f"y, eps {eps}")
+        dx, dw = _blank((6, H), F32), torch.empty(H, device="cuda")
+        ws = torch.empty(mg.rms_norm_bwd_workspace(6, H) // 4, device="cuda")
+        mg.rms_norm_bwd(dy, x, w, dx, grad_weight=dw, workspace=ws, eps=eps)
+        rx, rw, size, wsize = layer.rms_norm_bwd(_np(dy), _np(x), _np(w), float(np.float32(eps)))
+        _close(dx, rx, 104 * U * size + 1e-37, "grad_x")
+        _close(dw, rw, 130 * U * wsize + 1e-37, "grad_weight")
+
+
+def test_many_short_rows():
+    say("rms_norm of 2^22 + 5 rows of 8")
+    T = 2 ** 22 + 5
+    x, w = _rows(_gen(12), (T, 8), BF), _rows(_gen(13), (8,), F32)
+    y = _blank((T, 8), BF)
+    mg.rms_norm(x, w, y=y)
+    at = [0, 2 ** 21, 2 ** 22 - 1, 2 ** 22, T - 1]
+    want = layer.rms_norm(_np(x[at]), _np(w), 1e-6)
+    _close(y[at], want, (26 * U + 2.0 ** -8) * np.abs(want) + 1e-37, "y")
+    assert torch.isfinite(y).all()
+    dx, dw = _blank((T, 8), BF), torch.empty(8, device="cuda")
+    ws = torch.empty(mg.rms_norm_bwd_workspace(T, 8) // 4, device="cuda")
+    mg.rms_norm_bwd(y, x, w, dx, grad_weight=dw, workspace=ws)
+    assert torch.isfinite(dx).all()
+    rx, _, size, _ = layer.rms_norm_bwd(_np(y[at]), _np(x[at]), _np(w), 1e-6)
+    _close(dx[at], rx, 104 * U * size + 2.0 ** -8 * np.abs(rx) + 1e-37, "grad_x")
+    _, rw, _, wsize = layer.rms_norm_bwd(_np(y), _np(x), _np(w), 1e-6)
+    _close(dw, rw, (-(-T // 512) + 120) * U * wsize, "grad_weight")
+
+
 def test_what_is_not_finite_stays_in_its_row():
     say("rms_norm of rows with NaN and infinities")
     H = 640

@@ -147,6 +147,37 @@ def test_medium_tiles(form, sizes):
     _case(form, sizes, 1032, 512, F32, "in place")
 
 
+@pytest.mark.parametrize("form", ["nt", "nn", "tn"])
+def test_strides_of_a_single_row(form):
+    """The stride of a dimension of one is of no account; weights may be shared by all groups."""
+    say(f"{form} of one row, and of one matrix for all groups")
+    gen = _gen(31)
+    G, N, K = 3, 72, 128
+    call, ref = {"nt": (mg.m_grouped_bf16_gemm_nt_ragged, layer.ragged_nt), "nn": (mg.m_grouped_bf16_gemm_nn_ragged, layer.ragged_nn),
+                 "tn": (mg.k_grouped_bf16_gemm_tn, layer.ragged_tn)}[form]
+    off = torch.tensor([0, 0, 1, 1], dtype=torch.int32, device="cuda")
+    for stride in (0, 8, 1 << 40):
+        a = _rows(gen, (N if form == "tn" else K,), BF).as_strided((1, N if form == "tn" else K), (stride, 1))
+        if form == "tn":
+            b = _rows(gen, (K,), BF).as_strided((1, K), (stride, 1))
+            d = torch.empty(G, N, K, device="cuda")
+        else:
+            b = _rows(gen, (1, N, K) if form == "nt" else (1, K, N), BF).expand(G, -1, -1)
+            d = torch.empty(1, N, device="cuda")
+        call(a, b, d, off)
+        o = off.cpu().numpy()
+        want, size = ref(_np(a), _np(b), o, None), ref(np.abs(_np(a)), np.abs(_np(b)), o, None)
+        if form != "tn":
+            want, size = want[0], size[0]
+        _close(d, want, ((1 if form == "tn" else K) + 2) * U * size * (1 + 1e-6) + 1e-37, f"stride {stride}")
+    if form == "nt":  # one output column
+        b = _rows(gen, (G, 1, K), BF).as_strided((G, 1, K), (K, 8, 1))
+        d = torch.empty(1, 1, device="cuda")
+        call(a, b, d, off)
+        want, size = ref(_np(a), _np(b), o, None)[0], ref(np.abs(_np(a)), np.abs(_np(b)), o, None)[0]
+        _close(d, want, (K + 2) * U * size * (1 + 1e-6) + 1e-37, "one column")
+
+
 def test_offsets_out_of_range():
     say("offsets past the rows, negative, falling")
     gen = _gen(1)
