@@ -25,10 +25,11 @@
 // What bounds it: 32 groups of 1024 rows, 4096 x 7168, run at 1430 TFLOP/s (1340
 // the gradient of a), at which the card's power limit holds the clock near 1.75 GHz;
 // with groups of 267 to 1760 rows 1260, 12.5% of the tiles' rows being empty.  A
-// weight gradient of 2048 x 7168 over 1024 rows a group runs at 940: its tiles are
-// 16 slices long, and their stores (256 KB in FP32) and the first waits behind them
-// take a quarter of the time.  Few rows are bound by the weights' stream: 8 rows
-// in six groups of 4096 x 7168 read them at 6.0 TB/s.
+// weight gradient of 2048 x 7168 over 1024 rows a group runs at 960: its tiles are
+// 16 slices long, and their stores (256 KB in FP32), which the loads behind them wait
+// for, take a quarter of the time (without them 720 us for 1000).  Few rows are
+// bound by the weights' stream: 8 rows in six groups of 4096 x 7168 read them at 6.0
+// TB/s.
 
 #include <type_traits>
 
@@ -393,16 +394,39 @@ __global__ __launch_bounds__(T::NT, 2) void ragged_kernel(const RaggedArgs p) {
       }
     }
   };
-  // lane: output row lane % 16 of each fragment row and, PERM, 16 consecutive columns, else 4 of each fragment
+  // TN: a fragment row goes through LDS of the wave's own, so that the lanes of an instruction hold 4 whole rows of the
+  // wave's 64 columns and not 64 bytes of 16 rows (32 gradients of 2048 x 7168 in FP32 over 256 to 1760 rows 1081 us for
+  // 1143; exchanged between lanes in registers 1095).  Chunk c of row r lies at slot c ^ r.
+  constexpr bool WHOLE = LAY == RAGGED_TN;
+  static_assert(!WHOLE || T::FN == 4, "16 chunks a row");
+  __shared__ __attribute__((aligned(16))) f32x4 turn[WHOLE ? T::NW * 256 : 1];
+  auto whole_rows = [&](f32x4* v, int fr, int q) __attribute__((always_inline)) {
+    f32x4* own = turn + wave * 256;
+#pragma unroll
+    for (int f = 0; f < 4; ++f) own[fr * 16 + ((4 * f + q) ^ fr)] = v[f];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");  // (a wave's LDS accesses are done in their order)
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int f = 0; f < 4; ++f) v[f] = own[(4 * f + q) * 16 + (fr ^ (4 * f + q))];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+  };
+  // lane: output row lane % 16 of each fragment row and, PERM, 16 consecutive columns, else 4 of each fragment; TN: 4
+  // columns of four rows
   auto store = [&](const Tile& x, int fm) __attribute__((always_inline)) {
+    int l = lane;
+    asm volatile("" : "+v"(l));  // (what follows from it is formed here: kept, it costs registers that there are not)
+    const int fr = l & 15, q = l >> 4;
     const int64_t d_at = LAY == RAGGED_TN ? (int64_t)x.g * p.d_gs : 0, c_at = LAY == RAGGED_TN ? (int64_t)x.g * p.c_gs : 0;
 #pragma unroll
     for (int i = 0; i < T::FM; ++i) {
-      const int row = x.m0 + wm * 16 * fm + 16 * i + fr;
-      if (i >= fm || row >= x.m_end) continue;
+      if (i >= fm) continue;
+      if constexpr (WHOLE) whole_rows(acc[i], fr, q);
 #pragma unroll
       for (int f0 = 0; f0 < T::FN; f0 += RUN / 4) {
-        const int col = x.n0 + wn * T::TN + (PERM ? 16 * q : 16 * f0 + 4 * q);
+        const int row = x.m0 + wm * 16 * fm + 16 * i + (WHOLE ? 4 * f0 + q : fr);
+        if (row >= x.m_end) continue;
+        const int col = x.n0 + wn * T::TN + (PERM ? 16 * q : WHOLE ? 4 * fr : 16 * f0 + 4 * q);
         const int n = min(RUN, x.n_end - col);
         if (p.c != nullptr) add_c(&acc[i][f0], c_at + (int64_t)row * p.ldc + col, n);
         const int64_t at = d_at + (int64_t)row * p.ldd + col;
