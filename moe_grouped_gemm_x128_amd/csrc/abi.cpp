@@ -1940,7 +1940,8 @@ int ragged_common(int layout, const dg_tensor* a, const dg_tensor* b, const dg_t
   DG_TRY(check_no_alias(d, "d", b, "b"));
   DG_TRY(check_no_alias(d, "d", offsets, "offsets"));
   if (G == 0 || N == 0 || (tn ? K : M) == 0) return ok();
-  if (dgmi::ragged_tiles(layout, G, M, N, K) > (double)(INT32_MAX - 4096))
+  constexpr int64_t kMaxExtent = INT32_MAX - 1024;  // (a tile that begins inside ends below 2^31)
+  if (M > kMaxExtent || N > kMaxExtent || K > kMaxExtent || dgmi::ragged_tiles(layout, G, M, N, K) > (double)(INT32_MAX - 4096))
     return fail(DG_UNSUPPORTED, "%s: too many groups, rows and columns for one call", fname);
   dgmi::RaggedArgs p = {};
   p.a = static_cast<const uint16_t*>(a->data);

@@ -246,8 +246,11 @@ hipError_t with_row_shape(int64_t H, F f) {
   DGMI_ROW(64, 1);
   DGMI_ROW(64, 2);
   DGMI_ROW(256, 1);
-  if constexpr (BWD) DGMI_ROW(512, 1);
-  else DGMI_ROW(256, 2);
+  if constexpr (BWD) {
+    DGMI_ROW(512, 1);
+  } else {
+    DGMI_ROW(256, 2);
+  }
   DGMI_ROW(512, 2);
   DGMI_ROW(1024, 2);
 #undef DGMI_ROW

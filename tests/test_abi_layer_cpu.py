@@ -195,6 +195,13 @@ def test_ragged_refusals(form):
     assert "overlap" in no(INVALID, b=b[..., :1, :].expand(sb))
     assert "overlap" in no(INVALID, a=a.view(-1)[:8 * sa[0] + sa[1]].as_strided(sa, (8, 1)))
     no(UNSUPPORTED, a=_far(sa))
+    many = 2 ** 31 - 1
+    if form == "nt":
+        no(UNSUPPORTED, a=_t((1, 0), BF16), b=_t((G, many, 0), BF16), d=torch.empty((1, many), dtype=BF16))
+    if form == "nn":
+        no(UNSUPPORTED, a=_t((many, 0), BF16), b=_t((G, 0, 1), BF16), d=torch.empty((many, 1), dtype=BF16))
+    if form == "tn":
+        no(UNSUPPORTED, a=_t((0, many), BF16), b=_t((0, 1), BF16), d=torch.empty((1, many, 1), dtype=BF16), off=_t(2, I32))
     if form != "tn":
         no(UNSUPPORTED, a=_t((M, 96), BF16), b=_t((G, N, 96) if form == "nt" else (G, 96, N), BF16))
     _taken(call, a, b, d, off)
