@@ -91,6 +91,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(const Rms
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int at = (lane + i * NT) * 8;
+    if (at - (lane & 15) * 8 >= p.H) continue;  // (of the 16 lanes of a block; 9887 x 5120 with FP8 output @A@ us for 59)
     float w[8];
     load8(p.w, p.w_bf16, 0, at, p.H, p.w_vec, w);
 #pragma unroll
@@ -234,8 +235,8 @@ __global__ __launch_bounds__(1024) void rms_norm_bwd_weight_kernel(const float* 
 }
 
 // Lanes and chunks that hold a row of H: NT * NI * 8 >= H.  Forward: two chunks a lane past 2048 (16384 rows of 4096
-// with residual and codes 89 us, 512 lanes of one chunk 108), 512 lanes past 4096 (8192 x 7168 84 us, 256 lanes of
-// four chunks 95, 1024 of one 125).  The gradient has more to hold a chunk: one up to 4096 (16384 x 4096 97 us, 256
+// with residual and codes 89 us, 512 lanes of one chunk 108), three past 4096 (9887 x 5120 with codes 36 us, 512 lanes
+// of two 44), 512 lanes of two past 6144 (8192 x 7168 84 us, 256 lanes of four 95, 1024 of one 125).  The gradient has more to hold a chunk: one up to 4096 (16384 x 4096 97 us, 256
 // lanes of two 161), two past it (8192 x 7168 107 us, 1024 lanes of one 111).
 template <bool BWD, class F>
 hipError_t with_row_shape(int64_t H, F f) {
@@ -250,6 +251,7 @@ hipError_t with_row_shape(int64_t H, F f) {
     DGMI_ROW(512, 1);
   } else {
     DGMI_ROW(256, 2);
+    DGMI_ROW(256, 3);
   }
   DGMI_ROW(512, 2);
   DGMI_ROW(1024, 2);

@@ -394,11 +394,44 @@ __global__ __launch_bounds__(T::NT, 2) void ragged_kernel(const RaggedArgs p) {
       }
     }
   };
+  // c's first n values of four at `at`, as they are stored (TN)
+  auto load_c = [&](int64_t at, int n) __attribute__((always_inline)) {
+    i32x4 w = {0, 0, 0, 0};
+    if (p.c_f32) {
+      const float* c = static_cast<const float*>(p.c) + at;
+      if (n >= 4 && (reinterpret_cast<uintptr_t>(c) & 15) == 0) {
+        w = *reinterpret_cast<const i32x4*>(c);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e < n) w[e] = __float_as_int(c[e]);
+      }
+    } else {
+      const uint16_t* c = static_cast<const uint16_t*>(p.c) + at;
+      if (n >= 4 && (reinterpret_cast<uintptr_t>(c) & 7) == 0) {
+        const i32x2 t = *reinterpret_cast<const i32x2*>(c);
+        w[0] = t[0];
+        w[1] = t[1];
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (e < n) w[e / 2] |= (int)((uint32_t)c[e] << (16 * (e & 1)));
+      }
+    }
+    return w;
+  };
+  auto add_loaded = [&](f32x4& v, const i32x4& w) __attribute__((always_inline)) {
+    if (p.c_f32)
+      v += f32x4{__int_as_float(w[0]), __int_as_float(w[1]), __int_as_float(w[2]), __int_as_float(w[3])};
+    else
+      v += f32x4{__uint_as_float((uint32_t)w[0] << 16), __uint_as_float((uint32_t)w[0] & 0xffff0000u),
+                 __uint_as_float((uint32_t)w[1] << 16), __uint_as_float((uint32_t)w[1] & 0xffff0000u)};
+  };
   // TN: a fragment row goes through LDS of the wave's own, so that the lanes of an instruction hold 4 whole rows of the
   // wave's 64 columns and not 64 bytes of 16 rows (32 gradients of 2048 x 7168 in FP32 over 256 to 1760 rows 1081 us for
   // 1143; exchanged between lanes in registers 1095).  Chunk c of row r lies at slot c ^ r.
   constexpr bool WHOLE = LAY == RAGGED_TN;
-  static_assert(!WHOLE || T::FN == 4, "16 chunks a row");
+  static_assert(T::FN == 4, "16 chunks of four columns a fragment row");
   __shared__ __attribute__((aligned(16))) f32x4 turn[WHOLE ? T::NW * 256 : 1];
   auto whole_rows = [&](f32x4* v, int fr, int q) __attribute__((always_inline)) {
     f32x4* own = turn + wave * 256;
@@ -418,17 +451,38 @@ __global__ __launch_bounds__(T::NT, 2) void ragged_kernel(const RaggedArgs p) {
     asm volatile("" : "+v"(l));  // (what follows from it is formed here: kept, it costs registers that there are not)
     const int fr = l & 15, q = l >> 4;
     const int64_t d_at = LAY == RAGGED_TN ? (int64_t)x.g * p.d_gs : 0, c_at = LAY == RAGGED_TN ? (int64_t)x.g * p.c_gs : 0;
+    // TN: c is loaded a fragment row ahead, before the stores of the one at hand, so that its loads do not wait in turn
+    // with them: tiles may have few slices (64 of 178 x 3840 over 0 to 7 rows 84 us for 130; 32 of 2048 x 7168 over 256
+    // to 1760 1317 for 1547; NT and NN, whose tiles have more, lose 2 to 10%).  c may be d: a lane loads what it stores.
+    auto c_row = [&](int i, i32x4* w) __attribute__((always_inline)) {
+      const int col = x.n0 + wn * T::TN + 4 * fr;
+#pragma unroll
+      for (int f = 0; f < T::FN; ++f) {
+        w[f] = i32x4{0, 0, 0, 0};
+        const int row = x.m0 + wm * 16 * fm + 16 * i + 4 * f + q;
+        if (row < x.m_end && col < x.n_end) w[f] = load_c(c_at + (int64_t)row * p.ldc + col, x.n_end - col);
+      }
+    };
+    i32x4 cw[T::FN];
+    if (WHOLE && p.c != nullptr) c_row(0, cw);
 #pragma unroll
     for (int i = 0; i < T::FM; ++i) {
       if (i >= fm) continue;
-      if constexpr (WHOLE) whole_rows(acc[i], fr, q);
+      if constexpr (WHOLE) {
+        whole_rows(acc[i], fr, q);
+        if (p.c != nullptr) {
+#pragma unroll
+          for (int f = 0; f < T::FN; ++f) add_loaded(acc[i][f], cw[f]);
+          if (i + 1 < T::FM) c_row(i + 1, cw);
+        }
+      }
 #pragma unroll
       for (int f0 = 0; f0 < T::FN; f0 += RUN / 4) {
         const int row = x.m0 + wm * 16 * fm + 16 * i + (WHOLE ? 4 * f0 + q : fr);
         if (row >= x.m_end) continue;
         const int col = x.n0 + wn * T::TN + (PERM ? 16 * q : WHOLE ? 4 * fr : 16 * f0 + 4 * q);
         const int n = min(RUN, x.n_end - col);
-        if (p.c != nullptr) add_c(&acc[i][f0], c_at + (int64_t)row * p.ldc + col, n);
+        if (!WHOLE && p.c != nullptr) add_c(&acc[i][f0], c_at + (int64_t)row * p.ldc + col, n);
         const int64_t at = d_at + (int64_t)row * p.ldd + col;
         if constexpr (F32) {
           float* to = static_cast<float*>(p.d) + at;
