@@ -140,6 +140,23 @@ def test_large_tiles_of_weight_gradients(sizes, N, K):
     _case("tn", sizes, N, K, BF, F32, behind=2)
 
 
+@pytest.mark.parametrize("ct", [F32, BF])
+@pytest.mark.parametrize("sizes,N,K", [([40, 0, 200, 1, 64, 129], 2048, 2048), ([5, 70, 0, 1], 256, 384)])
+def test_weight_gradients_added_up(sizes, N, K, ct):
+    """Whole aligned rows: FP32 sums in place, and a BF16 C beside an FP32 D."""
+    say(f"tn groups {sizes} N={N} K={K} added to {ct}")
+    gen = _gen(N + K)
+    off = _offsets(sizes)
+    a, b = _rows(gen, (sum(sizes), N), BF), _rows(gen, (sum(sizes), K), BF)
+    c = _rows(gen, (len(sizes), N, K), ct, 4.0)
+    d = c if ct == F32 else torch.empty(len(sizes), N, K, device="cuda")
+    cn = _np(c)
+    mg.k_grouped_bf16_gemm_tn(a, b, d, off, c=c)
+    o = off.cpu().numpy()
+    want, size = layer.ragged_tn(_np(a), _np(b), o, cn), layer.ragged_tn(np.abs(_np(a)), np.abs(_np(b)), o, np.abs(cn))
+    _close(d, want, (max(sizes) + 2) * U * size * (1 + 1e-6), "d")
+
+
 @pytest.mark.parametrize("form", ["nt", "nn", "tn"])
 @pytest.mark.parametrize("sizes", [[900, 500, 0, 1100], [130] * 30])
 def test_medium_tiles(form, sizes):
