@@ -88,6 +88,15 @@ __device__ __forceinline__ float row_sum(float v, float* red) {
   return v;
 }
 
+// encode4 of values that are at most 448 scales (and of some that are not finite, whose codes do not matter): without
+// its clamp (6144 rows of 2048 through the activation 16.4 us for 17.3).  A quotient that rounds past 448 still rounds
+// to 448's code.
+__device__ __forceinline__ uint32_t encode4_in_range(const float v[4], Recip d) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(quot(v[0], d), quot(v[1], d), 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(quot(v[2], d), quot(v[3], d), w, true);
+  return (uint32_t)w;
+}
+
 // The FP8 cast of a 128-element block held by 16 lanes, eight elements each
 // (zeros past its end): the lane's codes, and the block's scale as every cast of
 // the library forms it.  As in the append to the cache, values that are not
@@ -108,8 +117,8 @@ __device__ __forceinline__ float cast_block8(const float v[8], int ue8m0, uint32
   }
   const float s = block_scale(amax, ue8m0);
   const Recip d = recip_of(s);
-  lo = encode4(v, d);
-  hi = encode4(v + 4, d);
+  lo = encode4_in_range(v, d);
+  hi = encode4_in_range(v + 4, d);
   if (odd != odd) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) {

@@ -11,7 +11,7 @@
 // 128-element block of the cast.
 //
 // What bounds it: memory for rows kept in BF16 (32749 x 2048, forward and gradient
-// together 1.07 GB in 184 us, 5.8 TB/s); with the cast about 25 vector instructions an
+// together 1.07 GB in 184 us, 5.8 TB/s); with the cast about 23 vector instructions an
 // element, half the time of 6144 rows of 2048 (16 us, 4.0 TB/s), whose bytes fit the
 // last cache.
 
