@@ -17,10 +17,11 @@
 //
 // What bounds it: memory.  Read once, written once: 16384 rows of 7168 with the
 // residual, its sum and FP8 codes (826 MB) take 161 us, 5.1 TB/s; 65536 x 1024
-// without them 41 us, 6.6 TB/s from the last cache.  The gradient holds the row, its
-// gradient, the weight and the weight's sums, so that 4 waves of 512-lane rows fit a
-// SIMD, and waits for a row's sums before it stores: 8192 x 4096 38 us (5.3 TB/s),
-// 8192 x 7168 96 us (3.7 TB/s); the weight's gradient adds 7 to 11 us.
+// without them 41 us, 6.6 TB/s from the last cache.  The gradient waits for a row's
+// sums before it stores; BF16 rows are kept packed and the next one is on its way
+// meanwhile: 8192 x 4096 with its weight's gradient and grad_h 48 us (5.6 TB/s; 56
+// without), 8192 x 7168 97 us (4.9 TB/s; 114).  F32 rows, loaded when their turn comes,
+// reach 5.2 TB/s.  The weight's gradient takes 5 to 7 us of that.
 
 #include <type_traits>
 
@@ -106,10 +107,21 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(const Rms
   }
 }
 
+// Eight BF16 values of a row as they are stored (zeros past its end); value e of them.
+__device__ __forceinline__ i32x4 raw8(const void* base, int64_t row, int at, int n) {
+  if (at >= n) return i32x4{0, 0, 0, 0};
+  return *reinterpret_cast<const i32x4*>(static_cast<const uint16_t*>(base) + row + at);
+}
+__device__ __forceinline__ float raw_value(const i32x4& v, int e) {
+  return __uint_as_float(e & 1 ? (uint32_t)v[e / 2] & 0xffff0000u : (uint32_t)v[e / 2] << 16);
+}
+
 // Rows blockIdx, + gridDim, ... of the gradient; the weight's sums stay in
-// registers and leave as one row of partial sums a workgroup.
-template <int NT, int NI>
-__global__ __launch_bounds__(NT < 256 ? 256 : NT, NT == 512 ? 4 : 1) void rms_norm_bwd_kernel(const RmsNormBwdArgs p) {
+// registers and leave as one row of partial sums a workgroup.  RAW: the inputs are
+// BF16, their rows whole 16-byte words: they stay packed, and the next row's are
+// loaded while this one's sums are made (16384 x 4096 83 us for 97, 65536 x 1024 87 for 97).
+template <int NT, int NI, bool RAW>
+__global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_bwd_kernel(const RmsNormBwdArgs p) {
   constexpr int RW = rows_of<NT>();
   __shared__ float red[NT / 64 + 1];
   __shared__ float sums[2][2][NT / 64 + 1];
@@ -124,22 +136,52 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT, NT == 512 ? 4 : 1) void rms_no
   }
   const int64_t step = (int64_t)gridDim.x * RW;
   int turn = 0;
-  for (int64_t row = (int64_t)blockIdx.x * RW + slot; row < p.rows; row += step, turn ^= 1) {
+  struct Row {
+    i32x4 x[NI], dy[NI], dh[NI];
+  };
+  auto load_row = [&](int64_t row, Row& v) __attribute__((always_inline)) {
     const int64_t i0 = row / p.heads, i1 = row - i0 * p.heads;
-    const int64_t oh = i0 * p.sh_0 + i1 * p.sh_1, og = i0 * p.sg_0 + i1 * p.sg_1;
-    float x[NI][8], dy[NI][8];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-      load8(p.h, p.h_bf16, oh, (lane + i * NT) * 8, p.H, p.h_vec, x[i]);
-      load8(p.dy, p.dy_bf16, og, (lane + i * NT) * 8, p.H, p.dy_vec, dy[i]);
+      const int at = (lane + i * NT) * 8;
+      v.x[i] = raw8(p.h, i0 * p.sh_0 + i1 * p.sh_1, at, p.H);
+      v.dy[i] = raw8(p.dy, i0 * p.sg_0 + i1 * p.sg_1, at, p.H);
+      v.dh[i] = raw8(p.dh, i0 * p.sd_0 + i1 * p.sd_1, at, p.dh != nullptr ? p.H : 0);
     }
+  };
+  Row ahead;
+  const int64_t first = (int64_t)blockIdx.x * RW + slot;
+  if (RAW && first < p.rows) load_row(first, ahead);
+  for (int64_t row = first; row < p.rows; row += step, turn ^= 1) {
+    const int64_t i0 = row / p.heads, i1 = row - i0 * p.heads;
+    const int64_t oh = i0 * p.sh_0 + i1 * p.sh_1, og = i0 * p.sg_0 + i1 * p.sg_1;
+    float xf[RAW ? 1 : NI][8], dyf[RAW ? 1 : NI][8];
+    Row here;
+    if constexpr (RAW) {
+      here = ahead;
+      if (row + step < p.rows) load_row(row + step, ahead);
+    } else {
+#pragma unroll
+      for (int i = 0; i < NI; ++i) {
+        load8(p.h, p.h_bf16, oh, (lane + i * NT) * 8, p.H, p.h_vec, xf[i]);
+        load8(p.dy, p.dy_bf16, og, (lane + i * NT) * 8, p.H, p.dy_vec, dyf[i]);
+      }
+    }
+    auto x = [&](int i, int e) __attribute__((always_inline)) {
+      if constexpr (RAW) return raw_value(here.x[i], e);
+      else return xf[i][e];
+    };
+    auto dy = [&](int i, int e) __attribute__((always_inline)) {
+      if constexpr (RAW) return raw_value(here.dy[i], e);
+      else return dyf[i][e];
+    };
     float s = 0.0f, m = 0.0f;
 #pragma unroll
     for (int i = 0; i < NI; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        s = __builtin_fmaf(x[i][e], x[i][e], s);
-        m = __builtin_fmaf(dy[i][e] * w[i][e], x[i][e], m);
+        s = __builtin_fmaf(x(i, e), x(i, e), s);
+        m = __builtin_fmaf(dy(i, e) * w[i][e], x(i, e), m);
       }
     s = lanes_sum<NT < 64 ? NT : 64>(s);
     m = lanes_sum<NT < 64 ? NT : 64>(m);
@@ -165,8 +207,8 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT, NT == 512 ? 4 : 1) void rms_no
       for (int i = 0; i < NI; ++i)
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
-          s += (x[i][e] * k) * (x[i][e] * k);
-          m += dy[i][e] * w[i][e] * (x[i][e] * k);
+          s += (x(i, e) * k) * (x(i, e) * k);
+          m += dy(i, e) * w[i][e] * (x(i, e) * k);
         }
       s = row_sum<NT>(s, red);
       m = row_sum<NT>(m, red);
@@ -179,12 +221,17 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT, NT == 512 ? 4 : 1) void rms_no
     for (int i = 0; i < NI; ++i) {
       const int at = (lane + i * NT) * 8;
       float dx[8];
-      load8(p.dh != nullptr ? p.dh : p.h, p.dh_bf16, od, at, p.dh != nullptr ? p.H : 0, p.dh_vec, dx);
+      if constexpr (RAW) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) dx[e] = raw_value(here.dh[i], e);
+      } else {
+        load8(p.dh != nullptr ? p.dh : p.h, p.dh_bf16, od, at, p.dh != nullptr ? p.H : 0, p.dh_vec, dx);
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float xh = (x[i][e] * k) * rk;
-        dw[i][e] = __builtin_fmaf(dy[i][e], xh, dw[i][e]);
-        dx[e] = __builtin_fmaf(r, __builtin_fmaf(-xh, mean, dy[i][e] * w[i][e]), dx[e]);
+        const float xh = (x(i, e) * k) * rk;
+        dw[i][e] = __builtin_fmaf(dy(i, e), xh, dw[i][e]);
+        dx[e] = __builtin_fmaf(r, __builtin_fmaf(-xh, mean, dy(i, e) * w[i][e]), dx[e]);
       }
       store8(p.dx, p.dx_bf16, ox, at, p.H, p.dx_vec, dx);
     }
@@ -236,8 +283,9 @@ __global__ __launch_bounds__(1024) void rms_norm_bwd_weight_kernel(const float* 
 
 // Lanes and chunks that hold a row of H: NT * NI * 8 >= H.  Forward: two chunks a lane past 2048 (16384 rows of 4096
 // with residual and codes 89 us, 512 lanes of one chunk 108), three past 4096 (9887 x 5120 with codes 36 us, 512 lanes
-// of two 44), 512 lanes of two past 6144 (8192 x 7168 84 us, 256 lanes of four 95, 1024 of one 125).  The gradient has more to hold a chunk: one up to 4096 (16384 x 4096 97 us, 256
-// lanes of two 161), two past it (8192 x 7168 107 us, 1024 lanes of one 111).
+// of two 44), 512 lanes of two past 6144 (8192 x 7168 84 us, 256 lanes of four 95, 1024 of one 125).
+// The gradient has more to hold a chunk, and takes one up to 8192 (16384 x 4096 97 us, 256 lanes of two 161; 16384 x
+// 7168 168 us, 512 of two 198).
 template <bool BWD, class F>
 hipError_t with_row_shape(int64_t H, F f) {
 #define DGMI_ROW(NT_, NI_) \
@@ -253,7 +301,11 @@ hipError_t with_row_shape(int64_t H, F f) {
     DGMI_ROW(256, 2);
     DGMI_ROW(256, 3);
   }
-  DGMI_ROW(512, 2);
+  if constexpr (BWD) {
+    DGMI_ROW(1024, 1);
+  } else {
+    DGMI_ROW(512, 2);
+  }
   DGMI_ROW(1024, 2);
 #undef DGMI_ROW
   return hipErrorInvalidValue;
@@ -272,11 +324,12 @@ int64_t rms_norm_max_rows(int64_t H) {
 }
 
 // Partial rows of the weight's gradient: workgroups of the gradient kernel.  Of 256 lanes four to a compute unit (32768
-// x 2048 94 us, two 147, three 108, eight 98), of 512 lanes two (8191 x 4096 62 us, three 71, four 67).
+// x 2048 94 us, two 147, three 108, eight 98), of 512 lanes two (8192 x 4096 43 us, three 47, four 48), of 1024 one
+// (16384 x 7168 168 us, two 175; 4096 x 16384 121, two 132).
 int64_t rms_norm_bwd_parts(int64_t rows, int64_t H) {
   const int64_t per = H <= 128 ? 16 : H <= 256 ? 8 : H <= 1024 ? 4 : 1;  // rows a workgroup takes side by side
   const int64_t groups = (rows + per - 1) / per;
-  const int64_t most = H <= 2048 ? 1024 : 512;
+  const int64_t most = H <= 2048 ? 1024 : H <= 4096 ? 512 : 256;
   return groups < most ? groups : most;
 }
 
@@ -293,7 +346,17 @@ hipError_t launch_rms_norm_bwd(const RmsNormBwdArgs& p, hipStream_t stream) {
   const int64_t parts = rms_norm_bwd_parts(p.rows, p.H);
   const hipError_t e = parts == 0 ? hipSuccess : with_row_shape<true>(p.H, [&](auto nt, auto ni) {
     constexpr int NT = decltype(nt)::value, NI = decltype(ni)::value;
-    rms_norm_bwd_kernel<NT, NI><<<dim3((unsigned)parts), dim3(NT < 256 ? 256 : NT), 0, stream>>>(p);
+    const bool raw = p.h_bf16 && p.dy_bf16 && p.h_vec && p.dy_vec && p.H % 8 == 0 &&
+                     (p.dh == nullptr || (p.dh_bf16 && p.dh_vec));
+    const dim3 gr((unsigned)parts), b(NT < 256 ? 256 : NT);
+    // (1024 lanes of two chunks: the packed rows spill; 64 of two with grad_h: 65536 x 1024 113 us for 108)
+    if constexpr (NT <= 64 || NI == 1) {
+      if (raw && (NI == 1 || p.dh == nullptr)) {
+        rms_norm_bwd_kernel<NT, NI, true><<<gr, b, 0, stream>>>(p);
+        return hipGetLastError();
+      }
+    }
+    rms_norm_bwd_kernel<NT, NI, false><<<gr, b, 0, stream>>>(p);
     return hipGetLastError();
   });
   if (e != hipSuccess || p.dw == nullptr) return e;
