@@ -148,6 +148,32 @@ def test_gradients(T, H, gt, ht, dt, wt):
             assert torch.equal(out, dx)
 
 
+@pytest.mark.parametrize("T,H", [(40000, 64), (9001, 256), (6001, 512), (5003, 1024), (2500, 2048), (1301, 4096), (600, 7168), (530, 16384)])
+@pytest.mark.parametrize("dt", [None, BF])
+def test_gradients_of_many_rows(T, H, dt):
+    """Several rows a workgroup, in place; a workgroup adds up at most ceil(T / 256) terms of a column."""
+    say(f"rms_norm_bwd T={T} H={H} grad_h {dt}")
+    gen = _gen(T + H)
+    dy, h, w = _rows(gen, (T, H), BF, 0.1), _rows(gen, (T, H), BF, 3.0), _rows(gen, (H,), F32)
+    dh = None if dt is None else _rows(gen, (T, H), dt, 0.1)
+    rx, rw, size, wsize = layer.rms_norm_bwd(_np(dy), _np(h), _np(w), 1e-3, None if dh is None else _np(dh))
+    ws = torch.full((mg.rms_norm_bwd_workspace(T, H) // 4,), float("nan"), device="cuda")
+    far = [_blank((T, H), BF, 8), _blank((T, H), BF, 1)]
+    dws = [torch.empty(H, device="cuda") for _ in range(3)]
+    for dx, dw in zip(far, dws):
+        mg.rms_norm_bwd(dy, h, w, dx, grad_weight=dw, workspace=ws, grad_h=dh, eps=1e-3)
+    _close(far[0], rx, 100 * U * size + HALF[BF] * np.abs(rx) + 1e-38, "grad_x")
+    _close(dws[0], rw, (-(-T // 256) + 120) * U * wsize + 1e-38, "grad_weight")
+    assert torch.equal(far[0], far[1]) and torch.equal(dws[0], dws[1])
+    # inputs whose rows are not whole 16-byte words, and in place
+    odd = torch.empty(T, H + 1, dtype=BF, device="cuda")[:, :H]
+    odd.copy_(h)
+    mg.rms_norm_bwd(dy, odd, w, odd, grad_weight=dws[2], workspace=ws, grad_h=dh, eps=1e-3)
+    assert torch.equal(odd, far[0]) and torch.equal(dws[2], dws[0])
+    mg.rms_norm_bwd(dy, h, w, h, grad_weight=dws[2], workspace=ws, grad_h=dh, eps=1e-3)
+    assert torch.equal(h, far[0]) and torch.equal(dws[2], dws[0])
+
+
 def test_rows_at_the_edges_of_fp32():
     say("rms_norm of rows of zeros, of the smallest and of the largest values")
     H = 300
