@@ -551,7 +551,8 @@ int rms_norm(const dg_tensor* x, const dg_tensor* weight, const dg_tensor* y, co
  *                between calls, but two calls that may run at once need one each
  *   grad_h       NULL, or F32 or BF16 of that shape: a gradient that reaches h
  *                from elsewhere (the residual stream), added to grad_x
- * FP32 sums in an order that depends on the sizes only.
+ * FP32 sums in an order that depends on the sizes only.  Rows and gradients may be
+ * of any size whose products grad_y weight and whose results FP32 holds.
  */
 int rms_norm_bwd(const dg_tensor* grad_y, const dg_tensor* h, const dg_tensor* weight, const dg_tensor* grad_x,
                  const dg_tensor* grad_weight, const dg_tensor* workspace, const dg_tensor* grad_h, float eps,

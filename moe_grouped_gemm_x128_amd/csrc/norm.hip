@@ -38,6 +38,14 @@ namespace {
 __device__ __forceinline__ bool out_of_range(float s, float eps) { return !(s < INFINITY) || (s < 0x1p-100f && eps < 0x1p-100f); }
 __device__ __forceinline__ float factor_of(float s) { return s < 0x1p-100f ? 0x1p96f : 0x1p-72f; }
 
+// The sum m of dy w h, made in one exchange with that of the squares, has left FP32's range where g xh need not: past
+// it, or so small that what the products lost below 2^-149 counts (with r up to 2^10 it stays below 2^-122 of grad_x).
+// It is then taken again of values that are normalised first, with their factor on g where the sum could overflow a
+// second time (16384 products of at most 2^128 2^-24 2^7).
+__device__ __forceinline__ bool products_out_of_range(float m, float mean, float r) {
+  return !(fabsf(m) < INFINITY) || !(fabsf(mean) < INFINITY) || (fabsf(m) < 0x1p-112f && r > 0x1p10f);
+}
+
 template <int NT>
 constexpr int rows_of() { return NT < 256 ? 256 / NT : 1; }  // rows a workgroup takes side by side
 
@@ -121,8 +129,9 @@ __device__ __forceinline__ float raw_value(const i32x4& v, int e) {
 // registers and leave as one row of partial sums a workgroup.  RAW: the inputs are
 // BF16, their rows whole 16-byte words: they stay packed, and the next row's are
 // loaded while this one's sums are made (16384 x 4096 83 us for 97, 65536 x 1024 87 for 97).
+// (Two chunks of 64 lanes unpacked take 129 registers unbidden: 65536 x 1024 168 us for 109 with 128.)
 template <int NT, int NI, bool RAW>
-__global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_bwd_kernel(const RmsNormBwdArgs p) {
+__global__ __launch_bounds__(NT < 256 ? 256 : NT, NT == 64 && NI == 2 && !RAW ? 4 : 1) void rms_norm_bwd_kernel(const RmsNormBwdArgs p) {
   constexpr int RW = rows_of<NT>();
   __shared__ float red[NT / 64 + 1];
   __shared__ float sums[2][2][NT / 64 + 1];
@@ -203,20 +212,27 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_bwd_kernel(const
     float k = 1.0f;
     if (out_of_range(s, p.eps)) {  // (the whole row takes this turn)
       k = factor_of(s);
-      s = m = 0.0f;
+      s = 0.0f;
 #pragma unroll
       for (int i = 0; i < NI; ++i)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          s += (x(i, e) * k) * (x(i, e) * k);
-          m += dy(i, e) * w[i][e] * (x(i, e) * k);
-        }
+        for (int e = 0; e < 8; ++e) s += (x(i, e) * k) * (x(i, e) * k);
       s = row_sum<NT>(s, red);
-      m = row_sum<NT>(m, red);
     }
     const float rk = __fdiv_rn(1.0f, __fsqrt_rn(__fdiv_rn(s, (float)p.H) + p.eps * k * k));
-    const float r = rk * k;                            // h r = (h k) rk
-    const float mean = __fdiv_rn(m * rk, (float)p.H);  // of g xh
+    const float r = rk * k;                      // h r = (h k) rk
+    float mean = __fdiv_rn(m * rk, (float)p.H);  // of g xh
+    if (k != 1.0f || products_out_of_range(m, mean, rk)) {  // (the whole row, too)
+      const float j = fabsf(m) < INFINITY ? 1.0f : 0x1p-24f;
+      float rr = rk;
+      asm volatile("" : "+v"(rr));  // (what follows from it is not kept for the outputs: there are no registers for it)
+      m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NI; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) m = __builtin_fmaf(dy(i, e) * w[i][e] * j, (x(i, e) * k) * rr, m);
+      mean = __fdiv_rn(row_sum<NT>(m, red), (float)p.H) * (1.0f / j);
+    }
     const int64_t od = i0 * p.sd_0 + i1 * p.sd_1, ox = i0 * p.sx_0 + i1 * p.sx_1;
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
