@@ -46,6 +46,17 @@ __device__ __forceinline__ bool products_out_of_range(float m, float mean, float
   return !(fabsf(m) < INFINITY) || !(fabsf(mean) < INFINITY) || (fabsf(m) < 0x1p-112f && r > 0x1p10f);
 }
 
+// a + b as FP32 holds it, one bit aside where the sum is not exact: rounded to BF16 next, a sum halfway between two
+// BF16 numbers goes to the side of the exact one.  (Two BF16 values need no such care: where FP32 cannot hold their sum,
+// the smaller of them does not lead near a middle.)
+__device__ __forceinline__ float sum_aside(float a, float b) {
+  const float s = a + b, c = s - a;
+  const float rest = (a - (s - c)) + (b - c);  // what the rounding left, exactly
+  const uint32_t bits = __float_as_uint(s);
+  if (!(fabsf(s) < INFINITY) || rest == 0.0f || (bits & 0xffff) != 0x8000) return s;
+  return __uint_as_float((rest < 0.0f) == (s < 0.0f) ? bits + 1 : bits - 1);
+}
+
 template <int NT>
 constexpr int rows_of() { return NT < 256 ? 256 / NT : 1; }  // rows a workgroup takes side by side
 
@@ -67,6 +78,18 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(const Rms
     for (int i = 0; i < NI; ++i) load8(p.res, p.r_bf16, orr, (lane + i * NT) * 8, p.H, p.r_vec, t[i]);
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
+      if (p.r_bf16 && !p.x_bf16) {
+        bool middle = false;  // is a sum, as FP32 holds it, halfway between two BF16 numbers?
+#pragma unroll
+        for (int e = 0; e < 8; ++e) middle |= (__float_as_uint(v[i][e] + t[i][e]) & 0xffff) == 0x8000;
+        if (middle) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            v[i][e] = sum_aside(v[i][e], t[i][e]);
+            t[i][e] = -0.0f;
+          }
+        }
+      }
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[i][e] += t[i][e];
       if (p.r_bf16) {  // the norm is of the sum as it is stored
