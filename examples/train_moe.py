@@ -58,6 +58,7 @@ class MoEBlock(torch.autograd.Function):
         return x + y
 
     @staticmethod
+    @torch.autograd.function.once_differentiable
     def backward(ctx, grad):
         (x, w_norm, w_router, w_up, w_down, h, logits, idx, rows, up, act, offsets, token, slot, row_weights,
          ones) = ctx.saved_tensors
