@@ -66,10 +66,10 @@ class MoEBlock(torch.autograd.Function):
         grad = grad.contiguous()
         d_down = grad[token]
         d_act = mg.m_grouped_bf16_gemm_nn_ragged(d_down, w_down, torch.empty_like(act), offsets)
-        dw_down = mg.k_grouped_bf16_gemm_tn(d_down, act, torch.empty_like(w_down, dtype=torch.float32), offsets)
+        dw_down = mg.k_grouped_bf16_gemm_tn(d_down, act, torch.empty_like(w_down), offsets)
         d_row_weights = torch.empty_like(row_weights)
         d_up = mg.swiglu_bwd(up, d_act, torch.empty_like(up), row_weights=row_weights, grad_row_weights=d_row_weights)
-        dw_up = mg.k_grouped_bf16_gemm_tn(d_up, rows, torch.empty_like(w_up, dtype=torch.float32), offsets)
+        dw_up = mg.k_grouped_bf16_gemm_tn(d_up, rows, torch.empty_like(w_up), offsets)
         d_rows = mg.m_grouped_bf16_gemm_nn_ragged(d_up, w_up, torch.empty_like(rows), offsets)
         d_h = mg.moe_combine(d_rows[None], slot, ones, _room(T, C)).float()
         d_logits = mg.moe_route_topk_bwd(logits, idx, d_row_weights[slot.long()], torch.empty_like(logits), score="sigmoid")
@@ -78,7 +78,7 @@ class MoEBlock(torch.autograd.Function):
         dx, dw_norm = torch.empty_like(x), _room(C, dtype=torch.float32)
         workspace = _room(mg.rms_norm_bwd_workspace(T, C) // 4, dtype=torch.float32)
         mg.rms_norm_bwd(d_h, x, w_norm, dx, grad_weight=dw_norm, workspace=workspace, grad_h=grad)
-        return dx, dw_norm, dw_router, dw_up.to(BF16), dw_down.to(BF16), None
+        return dx, dw_norm, dw_router, dw_up, dw_down, None
 
 
 def block_weights(C, E, I, gen):
