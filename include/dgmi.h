@@ -595,7 +595,9 @@ int swiglu_bwd(const dg_tensor* x, const dg_tensor* grad_y, const dg_tensor* gra
  * of the tokens' tensors (device memory, never read by the host; values are cut
  * to [0, M], a group whose end is not past its start is empty).  offsets is
  * expected not to fall: where it does, which rows of d are computed is not
- * specified.  FP32 accumulation.
+ * specified.  FP32 accumulation, in an order that depends on the group's index
+ * and b's sizes and strides (tn: on the group's rows) and on nothing else of the
+ * call: a row keeps its bits whatever the other groups hold.
  *   nt  d[m] = c[m] + a[m] . b[g]^T   a [M, K], b [G, N, K], d [M, N]: the
  *       forward product of m_grouped_bf16_gemm_nt_contiguous without its blocks
  *   nn  d[m] = c[m] + a[m] . b[g]     a [M, K], b [G, K, N], d [M, N]: the

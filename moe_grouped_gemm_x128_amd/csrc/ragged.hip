@@ -263,10 +263,15 @@ __global__ __launch_bounds__(T::NT, 2) void ragged_kernel(const RaggedArgs p) {
   Cols a_cols = {}, b_cols = {};
   auto load_from = [&](const Tile& x) __attribute__((always_inline)) {
     KB = (x.len + SLICE - 1) / SLICE;
-    // The XCDs begin with different slices where weight rows are a multiple of 4 KB apart: all at one, they would be at
-    // the same few channels of the memory.
+    // Where weight rows are a multiple of 4 KB apart, the XCDs begin with different slices: all at one, they would be at
+    // the same few channels of the memory.  An XCD's share of a round is 32 tiles of 256 columns in turn; which slice
+    // comes first hangs on the group and the columns alone, not on the XCD itself, so that a row's sum is of one order in
+    // every batch (runs of 16: 32 groups of 192 rows, 7168 x 2048 219 us for 224, of one row, 4096 x 4096 182 for 176).
     // (6144 rows of 7168 x 2048: 247 us for 255; without such rows 1% slower.)
-    if constexpr (LAY == RAGGED_NT) rot = p.ldb * 2 % 4096 == 0 ? (int)(blockIdx.x % XCDS) * KB / XCDS : 0;
+    if constexpr (LAY == RAGGED_NT) {
+      const int run = (x.g * ((p.N + 255) >> 8) + (x.n0 >> 8)) >> 5;
+      rot = p.ldb * 2 % 4096 == 0 ? run % XCDS * KB / XCDS : 0;
+    }
     const uint16_t* A = p.a + (A_MN ? (int64_t)x.first * p.lda + x.m0 : (int64_t)x.m0 * p.lda);
     const uint16_t* B = p.b + (LAY == RAGGED_TN ? (int64_t)x.first * p.ldb + x.n0
                                                 : (int64_t)x.g * p.b_gs + (B_MN ? (int64_t)x.n0 : (int64_t)x.n0 * p.ldb));
