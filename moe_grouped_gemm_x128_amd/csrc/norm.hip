@@ -20,8 +20,9 @@
 // residual, its sum and FP8 codes (826 MB) take 161 us, 5.1 TB/s; 65536 x 1024
 // without them 41 us, 6.6 TB/s from the last cache.  The gradient waits for a row's
 // sums before it stores; BF16 rows are kept packed and the next one is on its way
-// meanwhile: 8192 x 4096 with its weight's gradient and grad_h 48 us (5.6 TB/s; 56
-// without), 8192 x 7168 97 us (4.9 TB/s; 114).  F32 rows, loaded when their turn comes,
+// meanwhile: 8192 x 4096 with its weight's gradient and grad_h 57 us over three sets of
+// inputs (4.7 TB/s; 48 us where they stay in the last cache, 56 without the packing), 8192
+// x 7168 97 us (4.9 TB/s; 114).  F32 rows, loaded when their turn comes,
 // reach 5.2 TB/s.  The weight's gradient takes 5 to 7 us of that.
 
 #include <type_traits>
@@ -124,7 +125,7 @@ __global__ __launch_bounds__(NT < 256 ? 256 : NT) void rms_norm_kernel(const Rms
 #pragma unroll
   for (int i = 0; i < NI; ++i) {
     const int at = (lane + i * NT) * 8;
-    if (at - (lane & 15) * 8 >= p.H) continue;  // (of the 16 lanes of a block; 9887 x 5120 with FP8 output @A@ us for 59)
+    if (at - (lane & 15) * 8 >= p.H) continue;  // (of the 16 lanes of a block)
     float w[8];
     load8(p.w, p.w_bf16, 0, at, p.H, p.w_vec, w);
 #pragma unroll
@@ -324,8 +325,8 @@ __global__ __launch_bounds__(1024) void rms_norm_bwd_weight_kernel(const float* 
 // Lanes and chunks that hold a row of H: NT * NI * 8 >= H.  Forward: two chunks a lane past 2048 (16384 rows of 4096
 // with residual and codes 89 us, 512 lanes of one chunk 108), three past 4096 (9887 x 5120 with codes 36 us, 512 lanes
 // of two 44), 512 lanes of two past 6144 (8192 x 7168 84 us, 256 lanes of four 95, 1024 of one 125).
-// The gradient has more to hold a chunk, and takes one up to 8192 (16384 x 4096 97 us, 256 lanes of two 161; 16384 x
-// 7168 168 us, 512 of two 198).
+// The gradient has more to hold a chunk, and takes one up to 8192 (16384 x 4096, not packed, 97 us, 256 lanes of two
+// 161; packed 82; 16384 x 7168 168 us, 512 of two 198).
 template <bool BWD, class F>
 hipError_t with_row_shape(int64_t H, F f) {
 #define DGMI_ROW(NT_, NI_) \
@@ -364,7 +365,7 @@ int64_t rms_norm_max_rows(int64_t H) {
 }
 
 // Partial rows of the weight's gradient: workgroups of the gradient kernel.  Of 256 lanes four to a compute unit (32768
-// x 2048 94 us, two 147, three 108, eight 98), of 512 lanes two (8192 x 4096 43 us, three 47, four 48), of 1024 one
+// x 2048, not packed, 94 us, two 147, three 108, eight 98; packed 84), of 512 lanes two (8192 x 4096 43 us, three 47, four 48), of 1024 one
 // (16384 x 7168 168 us, two 175; 4096 x 16384 121, two 132).
 int64_t rms_norm_bwd_parts(int64_t rows, int64_t H) {
   const int64_t per = H <= 128 ? 16 : H <= 256 ? 8 : H <= 1024 ? 4 : 1;  // rows a workgroup takes side by side

@@ -22,14 +22,14 @@
 // kept in LDS; a group's last tile, where it is at most half full, is shared out
 // among all waves (2 to 3% over groups of 256 to 1760 rows).
 //
-// What bounds it: 32 groups of 1024 rows, 4096 x 7168, run at 1430 TFLOP/s (1340
-// the gradient of a), at which the card's power limit holds the clock near 1.75 GHz;
-// with groups of 267 to 1760 rows 1260, 12.5% of the tiles' rows being empty.  A
-// weight gradient of 2048 x 7168 over 1024 rows a group runs at 960: its tiles are
-// 16 slices long, and their stores (256 KB in FP32), which the loads behind them wait
-// for, take a quarter of the time (without them 720 us for 1000).  Few rows are
-// bound by the weights' stream: 8 rows in six groups of 4096 x 7168 read them at 6.0
-// TB/s.
+// What bounds it: 32 groups of 1024 rows, 4096 x 7168, run at 1400 to 1430 TFLOP/s
+// (the gradient of a at 1340 to 1360), at which the card's power limit holds the clock
+// near 1.75 GHz; with groups of 267 to 1760 rows 1150 to 1270, 12.5% of the tiles' rows
+// being empty.  A weight gradient of 2048 x 7168 over 1024 rows a group runs at 940 to
+// 960: its tiles are 16 slices long, and their stores (256 KB in FP32), which the loads
+// behind them wait for, take a quarter of the time (without them 720 us for 1000).  Few
+// rows are bound by the weights' stream: 8 rows in six groups of 4096 x 7168 read them at
+// 5.8 TB/s; one group's few rows by the time of a slice (256 rows of 4096 x 4096 21 us).
 
 #include <type_traits>
 
@@ -458,7 +458,7 @@ __global__ __launch_bounds__(T::NT, 2) void ragged_kernel(const RaggedArgs p) {
     const int64_t d_at = LAY == RAGGED_TN ? (int64_t)x.g * p.d_gs : 0, c_at = LAY == RAGGED_TN ? (int64_t)x.g * p.c_gs : 0;
     // TN: c is loaded a fragment row ahead, before the stores of the one at hand, so that its loads do not wait in turn
     // with them: tiles may have few slices (64 of 178 x 3840 over 0 to 7 rows 84 us for 130; 32 of 2048 x 7168 over 256
-    // to 1760 1317 for 1547; NT and NN, whose tiles have more, lose 2 to 10%).  c may be d: a lane loads what it stores.
+    // to 1760 1271 to 1317 for 1547; NT and NN, whose tiles have more, lose 2 to 10%).  c may be d: a lane loads what it stores.
     auto c_row = [&](int i, i32x4* w) __attribute__((always_inline)) {
       const int col = x.n0 + wn * T::TN + 4 * fr;
 #pragma unroll
