@@ -40,7 +40,7 @@ __device__ __forceinline__ bool out_of_range(float s, float eps) { return !(s < 
 __device__ __forceinline__ float factor_of(float s) { return s < 0x1p-100f ? 0x1p96f : 0x1p-72f; }
 
 // The sum m of dy w h, made in one exchange with that of the squares, has left FP32's range where g xh need not: past
-// it, or so small that what the products lost below 2^-149 counts (with r up to 2^10 it stays below 2^-122 of grad_x).
+// it, or so small that what the products lost below 2^-149 counts (with r up to 2^10 it is below 2^-122 in grad_x).
 // It is then taken again of values that are normalised first, with their factor on g where the sum could overflow a
 // second time (16384 products of at most 2^128 2^-24 2^7).
 __device__ __forceinline__ bool products_out_of_range(float m, float mean, float r) {
